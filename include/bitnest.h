@@ -383,6 +383,183 @@ int bitnest_spec_greedy(const bitnest_spec_model *model, int steps, int32_t *seq
                         int32_t *len, int32_t *stats, void *work, int64_t work_bytes,
                         void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and serving from a nested KV cache: a batch of sequences
+ * that share a prefix, with bounded caches.
+ * ---------------------------------------------------------------------- */
+
+/* Types of float arrays where an entry point takes both. */
+#define BITNEST_F16 0
+#define BITNEST_F32 1
+
+/* Which values of a head's first `rot` make a pair. */
+#define BITNEST_ROPE_HALF 0  /* i and i + rot / 2 */
+#define BITNEST_ROPE_PAIRS 1 /* 2 i and 2 i + 1   */
+
+/* Frequencies theta_i of the pairs i = 0 .. rot / 2 - 1, from
+ * theta_i = base^(-2 i / rot). */
+#define BITNEST_ROPE_PLAIN 0
+#define BITNEST_ROPE_LINEAR 1 /* theta_i / factor                                   */
+#define BITNEST_ROPE_NTK 2    /* with base * factor^(rot / (rot - 2))               */
+#define BITNEST_ROPE_BANDS 3  /* by turns over the trained length, n = trained theta_i / 2 pi:
+                                 theta_i (t + (1 - t) / factor),
+                                 t = clamp((n - low) / (high - low), 0, 1)           */
+#define BITNEST_ROPE_YARN 4   /* by pair: theta_i (1 - r + r / factor),
+                                 r = clamp((i - from) / (to - from), 0, 1) with from, to the
+                                 pairs that make `high`, `low` turns over the trained length
+                                 (rounded outwards); magnitude 0.1 ln(factor) + 1    */
+
+/*
+ * The phases of rotary positions (host only): phase[i] = theta_i / 2 pi * 2^64,
+ * the turns per position as a 64-bit fraction, rounded to nearest, for
+ * i < rot / 2; copy them to the device for the entry points below.
+ *   rot            : even, 2 .. 65536.   base : > 1.
+ *   scaling        : BITNEST_ROPE_PLAIN .. YARN; factor >= 1 (not read for
+ *                    PLAIN); low, high (0 < low < high) and trained (> 0
+ *                    positions) are read for BANDS and YARN.
+ *   phase          : HOST array of rot / 2.
+ *   magnitude      : HOST float, the factor m of the rotation.
+ */
+int bitnest_rope_phases(int64_t rot, double base, int scaling, double factor, double low,
+                        double high, int64_t trained, uint64_t *phase, float *magnitude);
+
+/*
+ * Rotary positions: every pair (a, b) of the first `rot` of D values of each
+ * head of token t becomes
+ *   m (a cos w - b sin w),  m (a sin w + b cos w),   w = pos[t] theta_i,
+ * the other D - rot values are copied.  The angle is exact modulo a turn at
+ * every int32 position (negative ones turn back).
+ *   x, y           : fp16 or fp32 each (x_type, y_type); element (t, h, d) at
+ *                    t * token stride + h * head stride + d (strides in
+ *                    elements).  Only the element type's alignment is
+ *                    required; 16-byte accesses are used where addresses and
+ *                    strides allow.  y may be x itself (same type and
+ *                    strides), else they must not overlap.
+ *   pos            : int32 [M] device.   phase : [rot / 2] device.
+ *   inverse        : non-zero turns by -w: with m = 1 the inverse, and for any
+ *                    m the transpose, that is the gradient of x from y's.
+ * rot even, 2 <= rot <= D <= 65536; strides are not negative, and y's rows lie
+ * by token (y_head >= D, y_token >= (heads - 1) y_head + D) or by head, else
+ * BITNEST_ERR_UNSUPPORTED_SHAPE.  M == 0 or heads == 0: nothing to do.
+ */
+int bitnest_rope(const void *x, int x_type, int64_t x_token, int64_t x_head, const int32_t *pos,
+                 const uint64_t *phase, float magnitude, int64_t M, int64_t heads, int64_t D,
+                 int64_t rot, int layout, int inverse, void *y, int y_type, int64_t y_token,
+                 int64_t y_head, void *stream);
+
+/*
+ * A nested KV cache: B sequences of up to `cap` tokens, rows of D = 128, row
+ * (b * cap + t) * Hkv + j = token t of sequence b, KV head j (planes uint8
+ * [B, cap, Hkv, 64], scales fp16 [B, cap, Hkv]): bitnest_pack_weights' rows,
+ * and with B = 1 the cache of bitnest_nested_attention.  The struct is a HOST
+ * struct of DEVICE pointers, 16-byte aligned.
+ */
+typedef struct bitnest_kv_cache {
+  uint8_t *k_hi;
+  uint8_t *k_lo;
+  uint16_t *k_scale;
+  uint8_t *v_hi;
+  uint8_t *v_lo;
+  uint16_t *v_scale;
+} bitnest_kv_cache;
+
+/*
+ * Append tokens: row start[b] + i of sequence b takes token i (of L) of its new
+ * keys and values, packed by bitnest_pack_weights' rule after rounding to fp16
+ * (values must be finite and within fp16's range; where a row's scale is
+ * subnormal and the high nibble would pass 7 it is clamped).
+ *   k, v           : fp16 or fp32 (type) [B, L, Hkv, 128]; token (b, i) starts
+ *                    at (b * L + i) * k_token (v_token) elements, a multiple of
+ *                    16 bytes and >= Hkv * 128.
+ *   start, count   : int32 [B] device.  count may be NULL (L each); tokens at
+ *                    or past count[b], and rows outside 0 .. cap - 1, are not
+ *                    written.
+ *   pos, phase     : as bitnest_rope's, pos [B, L]; the keys are turned before
+ *                    they are rounded (bit for bit what bitnest_rope and
+ *                    bitnest_pack_weights give).  phase NULL: not turned, pos
+ *                    not read.  rot a multiple of 16, 16 .. 128.
+ */
+int bitnest_kv_append(const void *k, int64_t k_token, const void *v, int64_t v_token, int type,
+                      int64_t B, int64_t L, int64_t Hkv, const int32_t *start,
+                      const int32_t *count, const int32_t *pos, const uint64_t *phase,
+                      float magnitude, int64_t rot, int layout, const bitnest_kv_cache *cache,
+                      int64_t cap, void *stream);
+
+/*
+ * Read rows back: k, v fp16 [B, L, Hkv, 128] = the draft's or the target's
+ * values of rows start[b] .. start[b] + L - 1 (start NULL: 0), rounded to
+ * nearest; rows outside the cache read as zeros.
+ */
+int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t cap, int64_t Hkv,
+                    const int32_t *start, int64_t L, uint16_t *k, uint16_t *v, void *stream);
+
+/*
+ * Attention of a batch that shares a prefix: query i (of L) of sequence b
+ * attends over all P tokens of `prefix` (a cache of one sequence) and over the
+ * tokens t <= len[b] - L + i of its own cache, that is, its L queries are the
+ * own cache's last L tokens:  out = sum_t p_t v_t,
+ * p = softmax(q k_t / sqrt(128)) with the draft's or the target's values.
+ *   q, out         : fp16 [B, L, H, 128]; head h reads KV head h / (H / Hkv).
+ *   len            : int32 [B] device, own tokens (at most cap are read).  A
+ *                    negative one leaves that sequence's out and lse as they
+ *                    were.  A query that sees nothing gets zeros and -inf.
+ *   lse            : fp32 [B, L, H], log sum_t exp(q k_t / sqrt(128)); or NULL.
+ *   prefix, own    : the lo planes are read for TARGET only; a cache of no
+ *                    tokens (P = 0, cap = 0) may be NULL.  Rows at or past
+ *                    len[b] may hold anything.
+ *   ws, ws_bytes   : device scratch of bitnest_prefix_attention_ws_bytes bytes
+ *                    (BITNEST_ERR_INVALID_ARG if fewer), 16-byte aligned; its
+ *                    contents do not matter.  Calls that run at the same time
+ *                    need scratch of their own (two graphs too, if they may).
+ * D must be 128, H / Hkv one of 1, 2, 4, 8.  The prefix is attended by all
+ * B * L * H / Hkv rows of a KV head together; its planes are read once for
+ * them, not once for each sequence.  Scores, statistics and sums are fp32; each
+ * p * v_scale enters its product rounded to fp16 (2^-12 of it at most), as the
+ * output is.  Results do not depend on timing.
+ */
+int64_t bitnest_prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
+                                          int64_t cap);
+int bitnest_prefix_attention(int mode, const uint16_t *q, int64_t B, int64_t L, int64_t H,
+                             int64_t Hkv, int64_t D, const bitnest_kv_cache *prefix, int64_t P,
+                             const bitnest_kv_cache *own, int64_t cap, const int32_t *len,
+                             uint16_t *out, float *lse, void *ws, int64_t ws_bytes, void *stream);
+
+/*
+ * The attention weight that cached tokens received, added up:
+ *   acc[b, j, t] += sum over queries i and heads h of KV head j that see token
+ *                   t of exp(q k_t / sqrt(128) - lse[b, i, h]).
+ *   len given      : each sequence's own cache (planes [B, cap, Hkv, 64], acc
+ *                    fp32 [B, Hkv, cap]); query i sees t <= len[b] - L + i.
+ *   len NULL       : one cache that all sequences see whole (planes
+ *                    [cap, Hkv, 64], acc fp32 [Hkv, cap]), the prefix.
+ *   q, lse         : bitnest_prefix_attention's; a query with lse = -inf gives
+ *                    no weight.  Values of acc at or past len[b] are left.
+ * B * Hkv <= 65535 where len is given.  Sums are fp32, in a fixed order.
+ */
+int bitnest_kv_weights(int mode, const uint16_t *q, const float *lse, int64_t B, int64_t L,
+                       int64_t H, int64_t Hkv, int64_t D, const uint8_t *k_hi, const uint8_t *k_lo,
+                       const uint16_t *k_scale, int64_t cap, const int32_t *len, float *acc,
+                       void *stream);
+
+/*
+ * Evict from a cache: of the n = min(len[b], cap) tokens of sequence b, each KV
+ * head keeps the first `sinks`, the last `recent` and, of those between, the
+ * ones of greatest acc (equal ones: the first; NaN counts as the least), `keep`
+ * in all, in their order; all of them where n <= keep.  They become rows
+ * 0, 1, .. of the sequence in the cache `dst` (rows behind them are left), and
+ *   kept           : int32 [B, Hkv, keep], their places in src, -1 behind them;
+ *   dst_acc        : fp32 [B, Hkv, dst_cap], their acc, 0 behind them;
+ *   dst_len        : int32 [B], min(n, keep).
+ * A negative len[b] leaves sequence b's rows and dst_acc as they were, with
+ * kept -1 and dst_len = len[b].  dst, dst_acc and dst_len must be other arrays
+ * than src, acc and len.  1 <= keep <= dst_cap, sinks + recent <= keep
+ * (else BITNEST_ERR_INVALID_ARG).
+ */
+int bitnest_kv_evict(const float *acc, const int32_t *len, int64_t B, int64_t Hkv, int64_t cap,
+                     int64_t keep, int64_t sinks, int64_t recent, const bitnest_kv_cache *src,
+                     const bitnest_kv_cache *dst, int64_t dst_cap, float *dst_acc, int32_t *kept,
+                     int32_t *dst_len, void *stream);
+
 /* The kernel family BITNEST_PATH_AUTO picks for this problem (host only,
  * launches nothing).  Returns BITNEST_PATH_GEMV or BITNEST_PATH_TC. */
 int bitnest_select_path(int mode, int64_t M, int64_t N, int64_t K);

@@ -47,6 +47,92 @@ bool hadamard_supported(int64_t K);
 cudaError_t launch_hadamard_quantize(const uint16_t *x, int64_t M, int64_t K, int8_t *xq,
                                      float *xs, int32_t *xsum, cudaStream_t st);
 
+// Rotary positions (x, y types: 0 fp16, 1 fp32).
+struct RopeArgs {
+  const void *x;
+  int x_type;
+  int64_t x_token, x_head;  // strides in elements
+  void *y;
+  int y_type;
+  int64_t y_token, y_head;
+  const int32_t *pos;     // [M]
+  const uint64_t *phase;  // [rot / 2]
+  float mag, sign;
+  int64_t M, heads, D, rot;
+  bool pairs;
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st);
+
+// Six planes of a nested KV cache, rows (b * cap + t) * Hkv + j.
+struct KvPlanes {
+  uint8_t *k_hi, *k_lo;
+  uint16_t *k_scale;
+  uint8_t *v_hi, *v_lo;
+  uint16_t *v_scale;
+};
+struct AppendArgs {
+  const void *k, *v;  // [B * L, Hkv, 128], token strides in elements
+  int type;
+  int64_t k_token, v_token;
+  const int32_t *start, *count, *pos;
+  const uint64_t *phase;  // null: the keys are turned already
+  float mag;
+  int64_t B, L, Hkv, cap, rot;
+  bool pairs;
+  KvPlanes cache;
+};
+cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t st);
+struct ReadArgs {
+  int mode;
+  const int32_t *start;  // null: 0
+  int64_t B, L, Hkv, cap;
+  KvPlanes cache;
+  uint16_t *k, *v;  // fp16 [B, L, Hkv, 128]
+};
+cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t st);
+
+// Attention of a batch over one prefix and each sequence's own tokens.
+struct PrefixAttnArgs {
+  int mode;
+  const uint16_t *q;  // fp16 [B, L, H, 128]
+  int64_t B, L, H, Hkv, P, cap;
+  KvPlanes prefix, own;
+  const int32_t *len;  // [B]
+  uint16_t *out;       // fp16 [B, L, H, 128]
+  float *lse;          // [B, L, H] or null
+  void *ws;
+};
+bool prefix_attention_supported(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
+                                int64_t cap);
+int64_t prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
+                                  int64_t cap);
+cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st);
+
+// Attention weight that each cached token received, added to acc [B, Hkv, cap]
+// (len null: acc [Hkv, cap], every query sees every token).
+struct KvWeightsArgs {
+  int mode;
+  const uint16_t *q;
+  const float *lse;
+  int64_t B, L, H, Hkv, cap;
+  const uint8_t *k_hi, *k_lo;
+  const uint16_t *k_scale;
+  const int32_t *len;
+  float *acc;
+};
+cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st);
+
+struct KvEvictArgs {
+  const float *acc;  // [B, Hkv, cap]
+  const int32_t *len;
+  int64_t B, Hkv, cap, cap_out, keep, sinks, recent;
+  KvPlanes src, dst;
+  float *acc_out;     // [B, Hkv, cap_out]
+  int32_t *kept;      // [B, Hkv, keep]
+  int32_t *len_out;   // [B]
+};
+cudaError_t launch_kv_evict(const KvEvictArgs &a, cudaStream_t st);
+
 // Largest M * K the GEMV kernels can stage in shared memory.
 bool gemv_fits(int64_t M, int64_t K);
 cudaError_t launch_gemv(const LinearArgs &a, cudaStream_t st);

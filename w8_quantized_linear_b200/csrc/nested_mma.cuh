@@ -1,0 +1,96 @@
+// mma.sync fragments of a nested cache's rows: the integer codes are exact in
+// fp16, so the tensor cores work on them and the row scales are applied in
+// fp32.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace bitnest {
+namespace nested {
+
+constexpr int kD = 128;  // head dimension (one scale group)
+
+// D = A (16x16 f16, row) * B (16x8 f16, col) + D, fp32
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte codes u of 8 columns from one 32-bit word of each plane: even columns
+// (the low nibbles) in `ev`, odd columns in `od`, byte b for plane byte b.
+// Draft: u = hi nibble; target: u = (hi << 4) | lo.
+template <int MODE>
+__device__ __forceinline__ void codes(uint32_t hw, uint32_t lw, uint32_t &ev, uint32_t &od) {
+  if (MODE == 0) {
+    ev = hw & 0x0F0F0F0Fu;
+    od = (hw >> 4) & 0x0F0F0F0Fu;
+  } else {
+    ev = ((hw << 4) & 0xF0F0F0F0u) | (lw & 0x0F0F0F0Fu);
+    od = (hw & 0xF0F0F0F0u) | ((lw >> 4) & 0x0F0F0F0Fu);
+  }
+}
+
+// fp16 pair (byte b of x, byte b of y) as codes u - offset: 0x6400 | u is the
+// half 1024 + u, and 1024 + u - (1024 + offset) is exact.
+template <int MODE>
+__device__ __forceinline__ uint32_t pair(uint32_t x, uint32_t y, int b) {
+  const uint32_t sel = (uint32_t)b | ((uint32_t)(b + 4) << 8);
+  const uint32_t t = (prmt(x, y, sel) & 0x00FF00FFu) | 0x64006400u;
+  constexpr uint32_t kOff = MODE ? 0xE488E488u : 0xE408E408u;  // -(1024 + offset)
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(kOff));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float half_bits(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Query rows of one KV head: row r is query r / G of the tile's first query
+// bi0 (a query is one token of one sequence) and head j * G + r % G.
+__device__ __forceinline__ int64_t query_row(int64_t bi0, int r, int G, int64_t H, int j) {
+  return (bi0 + r / G) * H + (int64_t)j * G + r % G;
+}
+
+// The A operand of the scores for row gid (p0) and gid + 8 (p1) of a 16-row
+// tile (null: zeros): k-step ks, K slots 2 tig, 2 tig + 1 <- columns
+// 32 tig + 4 ks + {0, 1}, slots 2 tig + 8, 2 tig + 9 <- + {2, 3}; a lane's
+// columns are then one 16-byte piece of each plane row.
+__device__ __forceinline__ void load_queries(uint32_t (&qa)[8][4], const uint16_t *p0,
+                                             const uint16_t *p1, int tig) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    const uint4 a = p0 ? __ldg(reinterpret_cast<const uint4 *>(p0 + 32 * tig) + i) : z;
+    const uint4 b = p1 ? __ldg(reinterpret_cast<const uint4 *>(p1 + 32 * tig) + i) : z;
+    qa[2 * i][0] = a.x;
+    qa[2 * i][1] = b.x;
+    qa[2 * i][2] = a.y;
+    qa[2 * i][3] = b.y;
+    qa[2 * i + 1][0] = a.z;
+    qa[2 * i + 1][1] = b.z;
+    qa[2 * i + 1][2] = a.w;
+    qa[2 * i + 1][3] = b.w;
+  }
+}
+
+}  // namespace nested
+}  // namespace bitnest

@@ -1,0 +1,428 @@
+// Attention of a batch of sequences that share a prefix, over nested KV
+// caches: query i of sequence b (of L) attends over the P prefix tokens, which
+// are stored once, and over its own cached tokens t <= len[b] - L + i,
+//   o = sum_t p_t v_t,  p = softmax(q k_t / sqrt(128)).
+//
+// The softmax is split by tokens: each part of the tokens gives its own
+// maximum, sum and output, and parts join by
+//   m = max m_s,  l = sum l_s 2^(m_s - m),  o = sum o_s l_s 2^(m_s - m) / l.
+// So the prefix is attended by all rows (queries x heads of a KV head) of the
+// batch together, as one product per KV head, and each sequence's own tokens
+// by its rows only; a second kernel joins the parts.
+#include "launch.h"
+#include "nested_mma.cuh"
+
+namespace bitnest {
+
+namespace pattn {
+
+using namespace nested;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;   // tokens a warp takes at a time
+constexpr int kRows = 16;   // rows of a warp
+constexpr int kMinExp = -40;  // below any fp16 scale / 16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
+
+struct Plan {
+  int G;              // query heads of a KV head
+  int row_warps;      // row tiles of a prefix CTA (its other warps split tokens)
+  int p_groups;       // prefix CTAs over the rows of a KV head
+  int p_splits, p_len;  // parts of the prefix, tokens of each
+  int o_tiles;        // row tiles of one sequence's rows
+  int o_splits, o_len;
+  int64_t p_ctas, o_ctas;
+};
+
+struct Smem {
+  float m[kWarps][kRows], l[kWarps][kRows];
+  float o[kWarps][kRows][kD];
+};
+
+struct TileRegs {
+  uint4 kh[2], kl[2];
+  uint2 vh[4], vl[4];
+  uint16_t ks[4], vs[4];
+};
+
+// One tile's loads for one lane (gid = lane / 4, tig = lane % 4): K rows of
+// tokens gid and 8 + gid (16 bytes of each plane at byte 16 tig), V rows of
+// tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9 (8 bytes at byte 8 gid), and
+// the scales of those four tokens.  Tokens at or past t_end read zeros.
+template <int MODE>
+__device__ __forceinline__ void load_tile(TileRegs &r, int t0, int t_end, int64_t row_base, int Hkv,
+                                          int gid, int tig, const KvPlanes &c) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int t = t0 + 8 * n + gid;
+    r.kh[n] = r.kl[n] = make_uint4(0, 0, 0, 0);
+    if (t < t_end) {
+      const int64_t off = (row_base + (int64_t)t * Hkv) * (kD / 2) + 16 * tig;
+      r.kh[n] = __ldg(reinterpret_cast<const uint4 *>(c.k_hi + off));
+      if (MODE) r.kl[n] = __ldg(reinterpret_cast<const uint4 *>(c.k_lo + off));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
+    r.vh[i] = r.vl[i] = make_uint2(0, 0);
+    r.ks[i] = r.vs[i] = 0;
+    if (t < t_end) {
+      const int64_t row = row_base + (int64_t)t * Hkv;
+      const int64_t off = row * (kD / 2) + 8 * gid;
+      r.vh[i] = __ldg(reinterpret_cast<const uint2 *>(c.v_hi + off));
+      if (MODE) r.vl[i] = __ldg(reinterpret_cast<const uint2 *>(c.v_lo + off));
+      r.ks[i] = __ldg(c.k_scale + row);
+      r.vs[i] = __ldg(c.v_scale + row);
+    }
+  }
+}
+
+// One part for a tile of 16 rows: tokens t_begin + 16 (first + n step) .. of
+// the rows' cache, row r seeing tokens below lim(r).  The state goes to slot
+// `warp` of the shared memory.
+template <int MODE>
+__device__ __forceinline__ void attend(Smem &sh, int warp, int lane, const KvPlanes &c,
+                                       int64_t row_base, int Hkv, int t_begin, int t_end,
+                                       int first, int step, const uint16_t *q0, const uint16_t *q1,
+                                       int lim0, int lim1) {
+  const int gid = lane >> 2, tig = lane & 3;
+  lim0 = min(lim0, t_end);
+  lim1 = min(lim1, t_end);
+  uint32_t qa[8][4];
+  load_queries(qa, q0, q1, tig);
+  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};  // rows gid, gid + 8
+  int e_run = kMinExp;             // o holds the output in units of 2^(e_run - 15)
+  float o[8][2][4];                // O^T: columns tile mt, rows tile nt
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
+
+  for (int t0 = t_begin + first * kTile; t0 < t_end; t0 += step * kTile) {
+    TileRegs cur;
+    load_tile<MODE>(cur, t0, t_end, row_base, Hkv, gid, tig, c);
+    float s[2][4];  // [row][token 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig]
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint32_t hw[4] = {cur.kh[n].x, cur.kh[n].y, cur.kh[n].z, cur.kh[n].w};
+      const uint32_t lw[4] = {cur.kl[n].x, cur.kl[n].y, cur.kl[n].z, cur.kl[n].w};
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t ev, od;
+        codes<MODE>(hw[w], lw[w], ev, od);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ks = 2 * w + h;
+          mma_f16(d, qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], pair<MODE>(ev, od, 2 * h),
+                  pair<MODE>(ev, od, 2 * h + 1));
+        }
+      }
+      s[0][2 * n] = d[0];
+      s[0][2 * n + 1] = d[1];
+      s[1][2 * n] = d[2];
+      s[1][2 * n + 1] = d[3];
+    }
+    float vf[4], vmax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
+      const float f = half_bits(cur.ks[i]) * (MODE ? 0.0625f * kScale : kScale);
+      // a token that a row does not see counts as -inf whatever its scale holds
+      s[0][i] = t < lim0 ? s[0][i] * f : -INFINITY;
+      s[1][i] = t < lim1 ? s[1][i] * f : -INFINITY;
+      vf[i] = half_bits(cur.vs[i]) * (MODE ? 0.0625f : 1.0f);
+      vmax = fmaxf(vmax, vf[i]);
+    }
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, x));
+    // 2^e: the largest v scale so far in [1/2, 1), times 2^15: p v_scale enters
+    // the product as one fp16 term (11 bits: 2^-12 of each weight at most, as
+    // the fp16 output's own rounding is), 2^29 above the fp16 subnormals
+    const int e_tile = vmax > 0.0f ? (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126 : kMinExp;
+    const int e_new = min(100, max(e_run, e_tile));
+    const float unit = pow2(max(e_run - e_new, -126));
+    const float down = pow2(15 - e_new);
+    e_run = e_new;
+    float corr[2];
+    uint32_t pb[2][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float tmax = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+      const float m_new = fmaxf(m_run[r], tmax);
+      const bool live = m_new != -INFINITY;  // a row that has seen a token
+      corr[r] = live ? exp2_approx(m_run[r] - m_new) : 1.0f;
+      float p[4], sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = s[r][i] != -INFINITY ? exp2_approx(s[r][i] - m_new) : 0.0f;
+        sum += p[i];
+        p[i] = s[r][i] != -INFINITY ? p[i] * (vf[i] * down) : 0.0f;
+      }
+      l_run[r] = l_run[r] * corr[r] + sum;  // this lane's tokens only
+      m_run[r] = m_new;
+      pb[r][0] = pack_half2(p[0], p[1]);
+      pb[r][1] = pack_half2(p[2], p[3]);
+    }
+    // rows 8 nt + 2 tig, + 1 of O^T's columns: their corr is in lanes 8 tig, 8 tig + 4
+    float cr[2][2];
+    bool rescale = false;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      cr[nt][0] = __shfl_sync(0xffffffffu, corr[nt], 8 * tig) * unit;
+      cr[nt][1] = __shfl_sync(0xffffffffu, corr[nt], 8 * tig + 4) * unit;
+      rescale |= cr[nt][0] != 1.0f || cr[nt][1] != 1.0f;
+    }
+    rescale = __any_sync(0xffffffffu, rescale);
+    uint32_t ev[4][2], od[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      codes<MODE>(cur.vh[i].x, cur.vl[i].x, ev[i][0], od[i][0]);
+      codes<MODE>(cur.vh[i].y, cur.vl[i].y, ev[i][1], od[i][1]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {  // plane byte 8 gid + mt: columns 16 gid + 2 mt, + 1
+      const int w = mt >> 2, b = mt & 3;
+      const uint32_t a0 = pair<MODE>(ev[0][w], ev[1][w], b);
+      const uint32_t a1 = pair<MODE>(od[0][w], od[1][w], b);
+      const uint32_t a2 = pair<MODE>(ev[2][w], ev[3][w], b);
+      const uint32_t a3 = pair<MODE>(od[2][w], od[3][w], b);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        if (rescale) {
+          o[mt][nt][0] *= cr[nt][0];
+          o[mt][nt][1] *= cr[nt][1];
+          o[mt][nt][2] *= cr[nt][0];
+          o[mt][nt][3] *= cr[nt][1];
+        }
+        mma_f16(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    if (tig == 0) {
+      sh.m[warp][gid + 8 * r] = m_run[r];
+      sh.l[warp][gid + 8 * r] = l_run[r];
+    }
+  }
+  const float up = pow2(e_run - 15);
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const int col = 16 * gid + 2 * mt;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float *o0 = sh.o[warp][8 * nt + 2 * tig], *o1 = sh.o[warp][8 * nt + 2 * tig + 1];
+      o0[col] = o[mt][nt][0] * up;
+      o1[col] = o[mt][nt][1] * up;
+      o0[col + 1] = o[mt][nt][2] * up;
+      o1[col + 1] = o[mt][nt][3] * up;
+    }
+  }
+}
+
+// The parts: CTAs below p_ctas take (KV head, row group, part of the prefix),
+// the others (sequence, KV head, row tile, part of its own tokens).
+// part_lse [parts, B L H] (in units of log 2), part_o [parts, B L H, 128].
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Plan pl,
+                                                            float *__restrict__ part_lse,
+                                                            float *__restrict__ part_o) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Smem &sh = *reinterpret_cast<Smem *>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2;
+  const int64_t H = a.H, rows_out = a.B * a.L * H;
+  const int Hkv = (int)a.Hkv, G = pl.G;
+  griddep_wait();
+  griddep_launch_dependents();
+  int64_t cta = blockIdx.x;
+  const bool prefix = cta < pl.p_ctas;
+  int j, row0, R, t_begin, t_end, ways, row_warps, part;
+  int64_t bi0, row_base;
+  int visible;  // own: tokens that the sequence's query 0 sees
+  if (prefix) {
+    const int split = (int)(cta % pl.p_splits);
+    cta /= pl.p_splits;
+    const int group = (int)(cta % pl.p_groups);
+    j = (int)(cta / pl.p_groups);
+    row_warps = pl.row_warps;
+    row0 = group * row_warps * kRows;
+    R = (int)(a.B * a.L) * G;
+    bi0 = 0;
+    row_base = j;
+    t_begin = split * pl.p_len;
+    t_end = min((int)a.P, t_begin + pl.p_len);
+    part = split;
+    visible = (int)a.P;
+  } else {
+    cta -= pl.p_ctas;
+    const int split = (int)(cta % pl.o_splits);
+    cta /= pl.o_splits;
+    const int tile = (int)(cta % pl.o_tiles);
+    cta /= pl.o_tiles;
+    j = (int)(cta % Hkv);
+    const int64_t b = cta / Hkv;
+    row_warps = 1;
+    row0 = tile * kRows;
+    R = (int)a.L * G;
+    bi0 = b * a.L;
+    row_base = b * a.cap * Hkv + j;
+    const int len = (int)min((int64_t)a.len[b], a.cap);
+    if (len < 0) return;  // the sequence is not taking part
+    t_begin = split * pl.o_len;
+    t_end = min(len, t_begin + pl.o_len);
+    part = pl.p_splits + split;
+    visible = len - (int)a.L + 1;
+  }
+  ways = kWarps / row_warps;
+  const int rw = warp % row_warps, way = warp / row_warps;
+  const int r0 = row0 + rw * kRows + gid, r1 = r0 + 8;
+  const uint16_t *q0 = r0 < R ? a.q + query_row(bi0, r0, G, H, j) * kD : nullptr;
+  const uint16_t *q1 = r1 < R ? a.q + query_row(bi0, r1, G, H, j) * kD : nullptr;
+  const int lim0 = r0 >= R ? 0 : prefix ? visible : visible + r0 / G;
+  const int lim1 = r1 >= R ? 0 : prefix ? visible : visible + r1 / G;
+  attend<MODE>(sh, warp, lane, prefix ? a.prefix : a.own, row_base, Hkv, t_begin, t_end, way, ways,
+               q0, q1, lim0, lim1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < row_warps * kRows * (kD / 4); e += kThreads) {
+    const int r = e / (kD / 4), c4 = e % (kD / 4), w0 = r / kRows, rr = r % kRows;
+    if (row0 + r >= R) continue;
+    float M = -INFINITY;
+    for (int w = 0; w < ways; ++w) M = fmaxf(M, sh.m[w0 + w * row_warps][rr]);
+    float den = 0.0f;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (M != -INFINITY)
+      for (int w = 0; w < ways; ++w) {
+        const int sw = w0 + w * row_warps;
+        if (sh.m[sw][rr] == -INFINITY) continue;
+        const float f = exp2_approx(sh.m[sw][rr] - M);
+        const float4 v = reinterpret_cast<const float4 *>(sh.o[sw][rr])[c4];
+        den += f * sh.l[sw][rr];
+        num.x += f * v.x;
+        num.y += f * v.y;
+        num.z += f * v.z;
+        num.w += f * v.w;
+      }
+    const int64_t at = (int64_t)part * rows_out + query_row(bi0, row0 + r, G, H, j);
+    if (c4 == 0) part_lse[at] = den > 0.0f ? M + log2f(den) : -INFINITY;
+    if (!(den > 0.0f)) continue;  // the join reads no output of a part without weight
+    const float inv = 1.0f / den;
+    reinterpret_cast<float4 *>(part_o + at * kD)[c4] =
+        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+  }
+}
+
+// One warp per output row.
+__global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, int parts,
+                                                   const float *__restrict__ part_lse,
+                                                   const float *__restrict__ part_o) {
+  const int64_t rows = a.B * a.L * a.H;
+  const int64_t row = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (row >= rows) return;
+  if (a.len[row / (a.L * a.H)] < 0) return;
+  float M = -INFINITY;
+  for (int s = 0; s < parts; ++s) M = fmaxf(M, part_lse[s * rows + row]);
+  float den = 0.0f, o[4] = {};
+  if (M != -INFINITY)
+    for (int s = 0; s < parts; ++s) {
+      const float ls = part_lse[s * rows + row];
+      if (ls == -INFINITY) continue;
+      const float f = exp2f(ls - M);
+      const float4 v = reinterpret_cast<const float4 *>(part_o + (s * rows + row) * kD)[lane];
+      den += f;
+      o[0] += f * v.x;
+      o[1] += f * v.y;
+      o[2] += f * v.z;
+      o[3] += f * v.w;
+    }
+  const float inv = den > 0.0f ? 1.0f / den : 0.0f;  // a row that sees nothing: zeros
+  const uint2 w = make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
+  reinterpret_cast<uint2 *>(a.out + row * kD)[lane] = w;
+  if (a.lse && lane == 0)
+    a.lse[row] = den > 0.0f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+}
+
+Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t cap) {
+  Plan p = {};
+  p.G = (int)(H / Hkv);
+  const int64_t R = B * L * p.G;
+  const int64_t tiles = (R + kRows - 1) / kRows;
+  p.row_warps = tiles >= 8 ? 8 : tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
+  p.p_groups = (int)((tiles + p.row_warps - 1) / p.row_warps);
+  const int step = kTile * (kWarps / p.row_warps);  // tokens a CTA takes at a time
+  if (P > 0) {
+    int64_t s = (2 * 148 + Hkv * p.p_groups - 1) / (Hkv * p.p_groups);
+    s = min(s, (P + 4 * step - 1) / (4 * step));
+    s = max((int64_t)1, min(s, (int64_t)64));
+    p.p_len = (int)(((P + s - 1) / s + step - 1) / step * step);
+    p.p_splits = (int)((P + p.p_len - 1) / p.p_len);
+  }
+  p.p_ctas = (int64_t)p.p_splits * p.p_groups * Hkv;
+  p.o_tiles = (int)((L * p.G + kRows - 1) / kRows);
+  if (cap > 0) {
+    const int64_t base = B * Hkv * p.o_tiles;
+    int64_t s = max((int64_t)1, (4 * 148 + base - 1) / base);
+    s = min(s, (cap + 255) / 256);
+    p.o_len = (int)(((cap + s - 1) / s + 127) / 128 * 128);
+    p.o_splits = (int)((cap + p.o_len - 1) / p.o_len);
+    p.o_ctas = base * p.o_splits;
+  }
+  return p;
+}
+
+}  // namespace pattn
+
+bool prefix_attention_supported(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
+                                int64_t cap) {
+  if (B < 0 || L < 1 || Hkv < 1 || H < Hkv || H % Hkv != 0 || P < 0 || cap < 0) return false;
+  const int64_t g = H / Hkv;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return false;
+  const int64_t lim = (int64_t)1 << 30;
+  if (B > lim || L > lim || H > 65535 || P > lim || cap > lim) return false;
+  if (B * L > lim / H || B * Hkv > (int64_t)1 << 22) return false;
+  if (B == 0) return true;
+  const pattn::Plan p = pattn::make_plan(B, L, H, Hkv, P, cap);
+  return p.p_ctas + p.o_ctas <= 0x7fffffff && (B * L * H + 7) / 8 <= 0x7fffffff;
+}
+
+int64_t prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
+                                  int64_t cap) {
+  if (B == 0) return 0;
+  const pattn::Plan p = pattn::make_plan(B, L, H, Hkv, P, cap);
+  const int64_t rows = (int64_t)(p.p_splits + p.o_splits) * B * L * H;
+  return (rows + 3) / 4 * 16 + rows * pattn::kD * 4;
+}
+
+cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
+  const pattn::Plan p = pattn::make_plan(a.B, a.L, a.H, a.Hkv, a.P, a.cap);
+  const int64_t out_rows = a.B * a.L * a.H;
+  const int64_t rows = (int64_t)(p.p_splits + p.o_splits) * out_rows;
+  float *lse = static_cast<float *>(a.ws);
+  float *o = lse + (rows + 3) / 4 * 4;
+  const int64_t ctas = p.p_ctas + p.o_ctas;
+  if (ctas > 0) {
+    auto kern = a.mode ? pattn::parts_kernel<1> : pattn::parts_kernel<0>;
+    constexpr int smem = (int)sizeof(pattn::Smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)ctas), dim3(pattn::kThreads), smem, st, true, a, p, lse, o);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(pattn::join_kernel, dim3((unsigned)((out_rows + 7) / 8)), dim3(256), 0, st,
+                    true, a, p.p_splits + p.o_splits, (const float *)lse, (const float *)o);
+}
+
+}  // namespace bitnest

@@ -107,6 +107,7 @@ bool prefix_attention_supported(int64_t B, int64_t L, int64_t H, int64_t Hkv, in
 int64_t prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
                                   int64_t cap);
 cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st);
+cudaError_t read_wait_timeout_prefix(int *flag, bool reset);
 
 // Attention weight that each cached token received, added to acc [B, Hkv, cap]
 // (len null: acc [Hkv, cap], every query sees every token).

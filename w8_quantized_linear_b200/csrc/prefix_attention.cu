@@ -11,6 +11,7 @@
 // by its rows only; a second kernel joins the parts.
 #include "launch.h"
 #include "nested_mma.cuh"
+#include "prefix_plan.h"
 
 namespace bitnest {
 
@@ -25,16 +26,6 @@ constexpr int kRows = 16;   // rows of a warp
 constexpr int kMinExp = -40;  // below any fp16 scale / 16
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
-
-struct Plan {
-  int G;              // query heads of a KV head
-  int row_warps;      // row tiles of a prefix CTA (its other warps split tokens)
-  int p_groups;       // prefix CTAs over the rows of a KV head
-  int p_splits, p_len;  // parts of the prefix, tokens of each
-  int o_tiles;        // row tiles of one sequence's rows
-  int o_splits, o_len;
-  int64_t p_ctas, o_ctas;
-};
 
 struct Smem {
   float m[kWarps][kRows], l[kWarps][kRows];
@@ -280,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Pl
     const int len = (int)min((int64_t)a.len[b], a.cap);
     if (len < 0) return;  // the sequence is not taking part
     t_begin = split * pl.o_len;
+    if (t_begin >= len) return;  // nor does the join read this part
     t_end = min(len, t_begin + pl.o_len);
     part = pl.p_splits + split;
     visible = len - (int)a.L + 1;
@@ -322,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Pl
   }
 }
 
-// One warp per output row.
-__global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, int parts,
+// One warp per output row: lane s holds the weights of parts s, s + 32, ..
+__global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, Plan pl,
                                                    const float *__restrict__ part_lse,
                                                    const float *__restrict__ part_o) {
   const int64_t rows = a.B * a.L * a.H;
@@ -332,27 +324,45 @@ __global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, int parts,
   griddep_wait();
   griddep_launch_dependents();
   if (row >= rows) return;
-  if (a.len[row / (a.L * a.H)] < 0) return;
+  const int64_t bi = row / a.H;
+  const int h = (int)(row - bi * a.H);
+  const int64_t len = min((int64_t)a.len[bi / a.L], a.cap);
+  if (len < 0) return;
+  // the parts of this row: np of the prefix, then those of its own tokens
+  int np = pl.p_splits;
+  if (pl.tc)
+    np = tc_parts(pl, (int64_t)(h / pl.G) * pl.tc_groups + (bi * pl.G + h % pl.G) / kTcRows);
+  const int own = pl.o_splits ? (int)((len + pl.o_len - 1) / pl.o_len) : 0;
+  const int parts = np + own;
+  auto slot = [&](int s) { return (int64_t)(s < np ? s : pl.p_splits + s - np) * rows + row; };
   float M = -INFINITY;
-  for (int s = 0; s < parts; ++s) M = fmaxf(M, part_lse[s * rows + row]);
+  for (int s = lane; s < parts; s += 32) M = fmaxf(M, part_lse[slot(s)]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float den = 0.0f, o[4] = {};
   if (M != -INFINITY)
-    for (int s = 0; s < parts; ++s) {
-      const float ls = part_lse[s * rows + row];
-      if (ls == -INFINITY) continue;
-      const float f = exp2f(ls - M);
-      const float4 v = reinterpret_cast<const float4 *>(part_o + (s * rows + row) * kD)[lane];
-      den += f;
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-      o[2] += f * v.z;
-      o[3] += f * v.w;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      const int n = min(32, parts - s0);
+      const float f = lane < n ? exp2f(part_lse[slot(s0 + lane)] - M) : 0.0f;
+#pragma unroll 4
+      for (int s = 0; s < n; ++s) {
+        const float w = __shfl_sync(0xffffffffu, f, s);
+        // the output of a part without weight is not written
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w != 0.0f) v = reinterpret_cast<const float4 *>(part_o + slot(s0 + s) * kD)[lane];
+        den += w;
+        o[0] += w * v.x;
+        o[1] += w * v.y;
+        o[2] += w * v.z;
+        o[3] += w * v.w;
+      }
     }
-  const float inv = den > 0.0f ? 1.0f / den : 0.0f;  // a row that sees nothing: zeros
+  // NaN scores give NaN; a row that sees nothing: zeros
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
   const uint2 w = make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
   reinterpret_cast<uint2 *>(a.out + row * kD)[lane] = w;
   if (a.lse && lane == 0)
-    a.lse[row] = den > 0.0f ? (M + log2f(den)) * 0.69314718055994531f : -INFINITY;
+    a.lse[row] = den == 0.0f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
 }
 
 Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t cap) {
@@ -363,14 +373,23 @@ Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t 
   p.row_warps = tiles >= 8 ? 8 : tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
   p.p_groups = (int)((tiles + p.row_warps - 1) / p.row_warps);
   const int step = kTile * (kWarps / p.row_warps);  // tokens a CTA takes at a time
-  if (P > 0) {
+  p.tc = P > 0 && R >= kTcMinRows;
+  if (p.tc) {
+    p.tc_groups = (int)((R + kTcRows - 1) / kTcRows);
+    p.tc_tiles = (int)((P + kTcTokens - 1) / kTcTokens);
+    p.tc_units = Hkv * p.tc_groups * p.tc_tiles;
+    p.tc_ctas = (int)min((int64_t)kSms, p.tc_units);
+    for (int64_t item = 0; item < Hkv * p.tc_groups; ++item)
+      p.p_splits = max(p.p_splits, tc_parts(p, item));
+    p.p_groups = 0;
+  } else if (P > 0) {
     int64_t s = (2 * 148 + Hkv * p.p_groups - 1) / (Hkv * p.p_groups);
     s = min(s, (P + 4 * step - 1) / (4 * step));
     s = max((int64_t)1, min(s, (int64_t)64));
     p.p_len = (int)(((P + s - 1) / s + step - 1) / step * step);
     p.p_splits = (int)((P + p.p_len - 1) / p.p_len);
   }
-  p.p_ctas = (int64_t)p.p_splits * p.p_groups * Hkv;
+  p.p_ctas = p.tc ? 0 : (int64_t)p.p_splits * p.p_groups * Hkv;
   p.o_tiles = (int)((L * p.G + kRows - 1) / kRows);
   if (cap > 0) {
     const int64_t base = B * Hkv * p.o_tiles;
@@ -395,7 +414,7 @@ bool prefix_attention_supported(int64_t B, int64_t L, int64_t H, int64_t Hkv, in
   if (B * L > lim / H || B * Hkv > (int64_t)1 << 22) return false;
   if (B == 0) return true;
   const pattn::Plan p = pattn::make_plan(B, L, H, Hkv, P, cap);
-  return p.p_ctas + p.o_ctas <= 0x7fffffff && (B * L * H + 7) / 8 <= 0x7fffffff;
+  return p.p_ctas + p.o_ctas <= 0x7fffffff && p.tc_units <= 0x3fffffff && (B * L * H + 7) / 8 <= 0x7fffffff;
 }
 
 int64_t prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
@@ -413,6 +432,10 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
   float *lse = static_cast<float *>(a.ws);
   float *o = lse + (rows + 3) / 4 * 4;
   const int64_t ctas = p.p_ctas + p.o_ctas;
+  if (p.tc) {
+    cudaError_t e = pattn::launch_prefix_tc(a, p, lse, o, st);
+    if (e != cudaSuccess) return e;
+  }
   if (ctas > 0) {
     auto kern = a.mode ? pattn::parts_kernel<1> : pattn::parts_kernel<0>;
     constexpr int smem = (int)sizeof(pattn::Smem);
@@ -422,7 +445,7 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(pattn::join_kernel, dim3((unsigned)((out_rows + 7) / 8)), dim3(256), 0, st,
-                    true, a, p.p_splits + p.o_splits, (const float *)lse, (const float *)o);
+                    true, a, p, (const float *)lse, (const float *)o);
 }
 
 }  // namespace bitnest

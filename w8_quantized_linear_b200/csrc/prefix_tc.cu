@@ -4,15 +4,17 @@
 // maximum.
 //
 // A CTA takes 256 rows of one KV head (two tiles, A and B) and 128 tokens at a
-// time, and an equal run of such units over all KV heads and row groups.  16
+// time, and an equal run of such units over all KV heads and row groups.  21
 // warps:
-//   0-7    softmax of tile A (0-3) and B (4-7), one row a thread: the scores
-//          from tensor memory, times the tokens' K scales, the row's running
-//          maximum, p = 2^(s - shift), times the V scales, rounded to fp16 and
-//          written back over the scores as the second product's A operand;
-//   8-11   the cache's codes as fp16 operands: plane words -> shared memory
+//   0-15   softmax of tile A (0-7) and B (8-15), 16 rows a warp, four threads a
+//          row (so that a token's scales serve two rows of a thread, and a
+//          thread needs a quarter of them): the scores from tensor memory,
+//          times the tokens' K scales, the row's running maximum,
+//          p = 2^(s - shift), times the V scales, rounded to fp16 and written
+//          back over the scores as the second product's A operand;
+//   16-19  the cache's codes as fp16 operands: plane words -> shared memory
 //          (128-byte swizzle), two stages of K and of V; the tokens' scales;
-//   12     issues the MMAs.
+//   20     issues the MMAs.
 // The tensor cores work on tile B while A is in its softmax and back.
 //
 // The codes are exact in fp16, so a score is off by fp32 sums only.  The
@@ -39,11 +41,9 @@ namespace {
 using namespace nested;
 
 constexpr int kRowsTile = 128, kRowsCta = 256, kTokens = 128;
-constexpr int kThreads = 512;
-constexpr int kLaunchRegs = 128;  // 512 threads x 128 = the SM's registers
-// after the split: 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128
-constexpr int kRegSoftmax = 184, kRegOperand = 96, kRegIssue = 48;
-static_assert(2 * kRegSoftmax + kRegOperand + kRegIssue == 4 * kLaunchRegs, "register split");
+constexpr int kSoftmaxWarps = 16, kOperandWarps = 4;
+constexpr int kIssueWarp = kSoftmaxWarps + kOperandWarps;
+constexpr int kThreads = (kSoftmaxWarps + kOperandWarps + 1) * 32;
 constexpr int kStages = 2, kSlots = 4;
 constexpr int kOperand = kTokens * kD * 2;  // bytes of a K, V or Q tile
 constexpr float kScale = 0.088388347648318440550f * 1.4426950408889634f;  // log2(e) / sqrt(128)
@@ -54,8 +54,11 @@ constexpr int kMinExp = -40;  // below any fp16 scale / 16
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kOperand;
 constexpr int kOffV = kOffK + kStages * kOperand;
-constexpr int kOffScale = kOffV + kStages * kOperand;        // [slot][k, v][128] floats
-constexpr int kOffExp = kOffScale + kSlots * 2 * kTokens * 4;  // [slot][4] ints
+// A slot's scales: token 8 n + 2 q + i at q * kScaleRow + 2 n + i, the order in which a
+// softmax thread holds its columns (its lane % 4 = q), rows in different banks
+constexpr int kScaleRow = 36, kScaleSet = 4 * kScaleRow;
+constexpr int kOffScale = kOffV + kStages * kOperand;        // [slot][k, v][kScaleSet] floats
+constexpr int kOffExp = kOffScale + kSlots * 2 * kScaleSet * 4;  // [slot][4] ints
 constexpr int kOffBar = kOffExp + kSlots * 4 * 4;
 constexpr int kBars = 4 * kStages + kSlots + 2 * 4 + 1;
 constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
@@ -99,29 +102,85 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(const void *base) {
   return d;
 }
 
-__device__ __forceinline__ void ld32(uint32_t taddr, float *r) {
+// 16 lanes x 64 columns: thread t gets of lane t / 4 the columns 8 n + 2 (t % 4), + 1 in
+// r[4 n], r[4 n + 1], and of lane t / 4 + 8 the same columns in r[4 n + 2], r[4 n + 3].
+__device__ __forceinline__ void ld_16x64(uint32_t taddr, float (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-        "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
-        "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]),
-        "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const float *r) {
+// 16 lanes x 8 columns, as above.
+__device__ __forceinline__ void ld_16x8(uint32_t taddr, float (&r)[4]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
-      "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]),
-      "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]),
-      "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]),
-      "f"(r[29]), "f"(r[30]), "f"(r[31])
+      "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+      : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void st_16x8(uint32_t taddr, const float (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3])
+               : "memory");
+}
+// 16 lanes x 32 columns: lane t / 4, column 4 n + t % 4 from r[2 n], lane t / 4 + 8 from r[2 n + 1].
+__device__ __forceinline__ void st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Wait for the loads issued so far; r passes through, so that nothing that uses
+// it can move in front.
+__device__ __forceinline__ void ld_wait32(float (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                 "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                 "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
+                 "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                 "+f"(r[30]), "+f"(r[31])::"memory");
+}
+
+// mbar_wait for waits that are short and frequent: no look at the timer before
+// some hundreds of tries.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (*(volatile int *)&g_wait_timeout) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) break;
+    }
+  }
+  atomicExch(&g_wait_timeout, 1);
+  return false;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(bar, parity));
+}
+
+__device__ __forceinline__ void f32x2_fma(float &d0, float &d1, float a0, float a1, float b0,
+                                          float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -147,46 +206,41 @@ __device__ __forceinline__ uint4 codes8(uint32_t hw, uint32_t lw) {
 }
 
 // One thread's share of a tile's plane rows: for q = 0 .. 3, 16 bytes (piece
-// tid % 4) of the row of token 32 q + tid / 4.
+// tid / 8 % 4) of the row of token 32 q + 8 (tid / 32) + tid % 8.
 struct Words {
   uint4 hi[4], lo[4];
 };
+struct Rows {  // where a thread's rows of a tile are
+  int64_t t, off;
+};
+__device__ __forceinline__ Rows rows_of(int64_t t0, int64_t Hkv, int j, int tid) {
+  const int64_t t = t0 + 8 * (tid >> 5) + (tid & 7);
+  return {t, (t * Hkv + j) * (kD / 2) + 16 * ((tid >> 3) & 3)};
+}
 template <int MODE>
-__device__ __forceinline__ void load_words(Words &w, const uint8_t *__restrict__ hi,
-                                           const uint8_t *__restrict__ lo, int64_t t0, int64_t P,
-                                           int64_t Hkv, int j, int tid) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t t = t0 + 32 * q + (tid >> 2);
-    w.hi[q] = w.lo[q] = make_uint4(0, 0, 0, 0);
-    if (t < P) {
-      const int64_t off = (t * Hkv + j) * (kD / 2) + 16 * (tid & 3);
-      w.hi[q] = __ldg(reinterpret_cast<const uint4 *>(hi + off));
-      if (MODE) w.lo[q] = __ldg(reinterpret_cast<const uint4 *>(lo + off));
-    }
+__device__ __forceinline__ void load_words(Words &w, int q, const uint8_t *__restrict__ hi,
+                                           const uint8_t *__restrict__ lo, const Rows &r,
+                                           int64_t P, int64_t Hkv) {
+  w.hi[q] = w.lo[q] = make_uint4(0, 0, 0, 0);
+  if (r.t + 32 * q < P) {
+    const int64_t off = r.off + q * 32 * Hkv * (kD / 2);
+    w.hi[q] = __ldg(reinterpret_cast<const uint4 *>(hi + off));
+    if (MODE) w.lo[q] = __ldg(reinterpret_cast<const uint4 *>(lo + off));
   }
 }
 // ... as fp16 to the tile at `dst`: token rows of 128 bytes in two halves (64
-// columns each, 16 KB apart), 16-byte chunk c of row t at c ^ (t % 8).  Pieces
-// 2 and 3 (the second half) take their words in the order 2 3 0 1, so that the
-// eight lanes of a store phase fall in different banks.
+// columns each, 16 KB apart), 16-byte chunk c of row t at c ^ (t % 8).  The
+// eight lanes of a store phase have tokens of different t % 8: different banks.
 template <int MODE>
-__device__ __forceinline__ void store_words(uint8_t *dst, const Words &w, int tid) {
-  const int piece = tid & 3;
-  const bool swap = piece >= 2;
+__device__ __forceinline__ void store_words(uint8_t *dst, const Words &w, int q, int tid) {
+  const int piece = (tid >> 3) & 3, t = 8 * (tid >> 5) + (tid & 7);
+  uint8_t *row = dst + (piece >> 1) * (kOperand / 2) + (t + 32 * q) * 128;
+  const uint32_t h[4] = {w.hi[q].x, w.hi[q].y, w.hi[q].z, w.hi[q].w};
+  const uint32_t l[4] = {w.lo[q].x, w.lo[q].y, w.lo[q].z, w.lo[q].w};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int t = 32 * q + (tid >> 2);
-    uint8_t *row = dst + (piece >> 1) * (kOperand / 2) + t * 128;
-    const uint32_t h[4] = {w.hi[q].x, w.hi[q].y, w.hi[q].z, w.hi[q].w};
-    const uint32_t l[4] = {w.lo[q].x, w.lo[q].y, w.lo[q].z, w.lo[q].w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t hw = swap ? h[c ^ 2] : h[c], lw = MODE ? (swap ? l[c ^ 2] : l[c]) : 0u;
-      const int chunk = ((piece & 1) * 4 + (swap ? c ^ 2 : c)) ^ (t & 7);
-      *reinterpret_cast<uint4 *>(row + chunk * 16) = codes8<MODE>(hw, lw);
-    }
-  }
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4 *>(row + ((((piece & 1) * 4 + c) ^ (t & 7)) << 4)) =
+        codes8<MODE>(h[c], l[c]);
 }
 
 struct Units {  // a CTA's run of units, one row group (item) at a time
@@ -206,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
                                                                 float *__restrict__ part_lse,
                                                                 float *__restrict__ part_o) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an integer cast would lose the address space)
   float *scales = reinterpret_cast<float *>(sm + kOffScale);
   int *exps = reinterpret_cast<int *>(sm + kOffExp);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
@@ -229,14 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
     }
     for (int s = 0; s < kSlots; ++s) mbar_init(&sc_full[s], 4);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 4);
+      mbar_init(&q_full[x], kSoftmaxWarps / 2);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[x], kSoftmaxWarps / 2);
       mbar_init(&o_done[x], 1);
     }
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
@@ -253,11 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   un.end = (int)((blockIdx.x + 1) * pl.tc_units / pl.tc_ctas);
   int item, t0, n;
 
-  if (warp < 8) {
-    setmaxnreg_inc<kRegSoftmax>();
-    const int x = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
-    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
-    const uint32_t ts = tmem + lane_base + kColS + 128 * x, to = tmem + lane_base + kColO + 128 * x;
+  if (warp < kSoftmaxWarps) {
+    // tile x; rows 32 (warp % 4) + 16 (warp / 4 % 2) .. + 15 of it, this
+    // thread's: lane / 4 and lane / 4 + 8 of those
+    const int x = warp >> 3, first_row = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+    const uint32_t ts = tmem + ((uint32_t)first_row << 16) + kColS + 128 * x,
+                   to = tmem + ((uint32_t)first_row << 16) + kColO + 128 * x;
     int it = 0, sx = 0;  // tiles of the CTA, tiles of this row tile
     bool ok = true;
     while (ok && un.next(item, t0, n)) {
@@ -267,16 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         it += n;
         continue;
       }
-      const int r = first + row;
-      const int64_t out_row = r < R ? query_row(0, r, G, a.H, j) : 0;
-      {  // the row's query in the operand's order
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + out_row * kD);
-        uint8_t *dst = sm + kOffQ + x * kOperand + row * 128;
+      {  // half of a row's query for each thread, in the operand's order
+        const int row = first_row + (lane >> 1), r = first + row, half = lane & 1;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+                               a.q + (r < R ? query_row(0, r, G, a.H, j) : 0) * kD) + 8 * half;
+        uint8_t *dst = sm + kOffQ + x * kOperand + half * (kOperand / 2) + row * 128;
 #pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 8; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (r < R) v = __ldg(src + c);
-          *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kOperand / 2) + (((c & 7) ^ (row & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) =
               make_uint4(prmt(v.x, v.y, 0x5410), prmt(v.z, v.w, 0x5410), prmt(v.x, v.y, 0x7632),
                          prmt(v.z, v.w, 0x7632));
         }
@@ -285,84 +340,115 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[x]);
 
-      float m = 0.0f, shift = 0.0f, sum0 = 0.0f, sum1 = 0.0f;
+      float m[2], shift[2], sum[2][2];
       int e = kMinExp;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) m[r] = shift[r] = sum[r][0] = sum[r][1] = 0.0f;
       for (int i = 0; i < n; ++i, ++it, ++sx) {
         const int slot = it & (kSlots - 1);
-        const float *ks = scales + slot * 2 * kTokens, *vs = ks + kTokens;
+        const float *ks = scales + slot * 2 * kScaleSet + (lane & 3) * kScaleRow, *vs = ks + kScaleSet;
         // the scores first: a tile that skipped row groups is then no further
         // than one phase from the scales' barrier, which has no count of its own
-        ok = mbar_wait_warp(&s_full[x], sx & 1) && mbar_wait_warp(&sc_full[slot], (it / kSlots) & 1);
+        ok = wait_warp(&s_full[x], sx & 1) && wait_warp(&sc_full[slot], (it / kSlots) & 1);
         if (!ok) break;
         tc_fence_after();
-        float t[128];
+        const int left = (int)a.P - (t0 + i) * kTokens;
+        if (left < kTokens) {  // the prefix ends inside the tile: its scales there are 1 and 0
+          for (int c = left >> 3; c < kTokens / 8; ++c) {
+            float o[4];
+            ld_16x8(ts + 8 * c, o);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, t + 32 * c);
-        tmem_ld_wait();
-        float tm = -INFINITY, tn = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          const float4 k4 = *reinterpret_cast<const float4 *>(ks + c);
-          f32x2_mul(t[c], t[c + 1], t[c], t[c + 1], k4.x, k4.y);
-          f32x2_mul(t[c + 2], t[c + 3], t[c + 2], t[c + 3], k4.z, k4.w);
+            for (int k = 0; k < 4; ++k)
+              o[k] = 8 * c + 2 * (lane & 3) + (k & 1) < left ? o[k] : -INFINITY;
+            st_16x8(ts + 8 * c, o);
+          }
+          tmem_st_wait();
         }
-        const int64_t left = a.P - (int64_t)(t0 + i) * kTokens;
-        if (left < kTokens) {  // the prefix ends inside the tile
+        // first pass: the maximum; the second reads the scores once more, so
+        // that 64 tokens are all that registers hold
+        float t[32], tm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 128; ++c) t[c] = c < left ? t[c] : -INFINITY;
-        }
+        for (int g = 0; g < 2; ++g) {
+          ld_16x64(ts + 64 * g, t);
+          ld_wait32(t);
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          tm = max3(tm, t[c], t[c + 1]);
-          tn = max3(tn, t[c + 2], t[c + 3]);
+          for (int k = 0; k < 4; ++k) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * g + 4 * k);
+            float *p = t + 8 * k;
+            f32x2_mul(p[0], p[1], p[0], p[1], k4.x, k4.y);
+            f32x2_mul(p[2], p[3], p[2], p[3], k4.x, k4.y);
+            f32x2_mul(p[4], p[5], p[4], p[5], k4.z, k4.w);
+            f32x2_mul(p[6], p[7], p[6], p[7], k4.z, k4.w);
+            tm[0] = max3(tm[0], p[0], p[1]);
+            tm[1] = max3(tm[1], p[2], p[3]);
+            tm[0] = max3(tm[0], p[4], p[5]);
+            tm[1] = max3(tm[1], p[6], p[7]);
+          }
         }
-        tm = fmaxf(tm, tn);
+        ld_16x64(ts, t);
         const int4 e4 = *reinterpret_cast<const int4 *>(exps + 4 * slot);
         const int e_new = max(max(e, max(e4.x, e4.y)), max(e4.z, e4.w));
+        bool grown = e_new > e;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          tm[r] = fmaxf(tm[r], __shfl_xor_sync(0xffffffffu, tm[r], 1));
+          tm[r] = fmaxf(tm[r], __shfl_xor_sync(0xffffffffu, tm[r], 2));
+          grown |= tm[r] > m[r] + kSlack;
+        }
         if (i == 0) {
-          m = tm;
           e = e_new;
-          shift = m + (float)(e - kHead);
-        } else if (__any_sync(0xffffffffu, tm > m + kSlack || e_new > e)) {
-          if (tm > m + kSlack) m = tm;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            m[r] = tm[r];
+            shift[r] = m[r] + (float)(e - kHead);
+          }
+        } else if (__any_sync(0xffffffffu, grown)) {
           e = e_new;
-          const float s_new = m + (float)(e - kHead);
-          const float f = exp2_approx(shift - s_new);
-          shift = s_new;
-          sum0 *= f;
-          sum1 *= f;
-          ok = mbar_wait_warp(&o_done[x], (sx - 1) & 1);  // the output so far is complete
+          float f[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (tm[r] > m[r] + kSlack) m[r] = tm[r];
+            const float s_new = m[r] + (float)(e - kHead);
+            f[r] = exp2_approx(shift[r] - s_new);
+            shift[r] = s_new;
+            sum[r][0] *= f[r];
+            sum[r][1] *= f[r];
+          }
+          ok = wait_warp(&o_done[x], (sx - 1) & 1);  // the output so far is complete
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            ld32(to + 32 * c, o);
-            tmem_ld_wait();
+          for (int c = 0; c < kD / 8; ++c) {
+            float o[4];
+            ld_16x8(to + 8 * c, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            st32(to + 32 * c, o);
+            for (int k = 0; k < 4; ++k) o[k] *= f[k >> 1];
+            st_16x8(to + 8 * c, o);
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int g = 0; g < 2; ++g) {
+          ld_wait32(t);
           uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float *p = t + 32 * c + k;
-            f32x2_sub(p[0], p[1], p[0], p[1], shift, shift);
-            f32x2_sub(p[2], p[3], p[2], p[3], shift, shift);
+          for (int k = 0; k < 4; ++k) {
+            float *p = t + 8 * k;
+            const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * g + 4 * k);
+            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 16 * g + 4 * k);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) p[q] = exp2_approx(p[q]);
-            f32x2_add(sum0, sum1, sum0, sum1, p[0], p[1]);
-            f32x2_add(sum0, sum1, sum0, sum1, p[2], p[3]);
-            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 32 * c + k);
-            f32x2_mul(p[0], p[1], p[0], p[1], v4.x, v4.y);
-            f32x2_mul(p[2], p[3], p[2], p[3], v4.z, v4.w);
-            pk[k / 2] = pack_half2(p[0], p[1]);
-            pk[k / 2 + 1] = pack_half2(p[2], p[3]);
+            for (int q = 0; q < 8; q += 2) {  // row lane / 4 + 8 (q / 2 % 2), two tokens
+              const int r = (q >> 1) & 1;
+              f32x2_fma(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? k4.x : k4.z, q < 4 ? k4.y : k4.w,
+                        -shift[r], -shift[r]);
+              p[q] = exp2_approx(p[q]);
+              p[q + 1] = exp2_approx(p[q + 1]);
+              f32x2_add(sum[r][0], sum[r][1], sum[r][0], sum[r][1], p[q], p[q + 1]);
+              f32x2_mul(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? v4.x : v4.z, q < 4 ? v4.y : v4.w);
+              pk[4 * k + q / 2] = pack_half2(p[q], p[q + 1]);
+            }
           }
-          tmem_st16(ts + 16 * c, pk);
+          if (g == 0) ld_16x64(ts + 64, t);  // behind the columns that the weights overwrite
+          st_16x32(ts + 32 * g, pk);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -370,155 +456,189 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      ok = mbar_wait_warp(&o_done[x], (sx - 1) & 1);
+      ok = wait_warp(&o_done[x], (sx - 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const float sum = sum0 + sum1, inv = 1.0f / sum;
-      const int64_t at = (blockIdx.x - tc_cta_of(pl, (int64_t)item * pl.tc_tiles)) * rows_out + out_row;
-      if (r < R) part_lse[at] = shift + log2f(sum);
-      float4 *dst = reinterpret_cast<float4 *>(part_o + at * kD);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        ld32(to + 32 * c, o);
-        tmem_ld_wait();
-        if (r < R)
+      const int64_t part = (blockIdx.x - tc_cta_of(pl, (int64_t)item * pl.tc_tiles)) * rows_out;
+      float inv[2];
+      float *dst[2];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            const float *p = o + k;
-            dst[8 * c + k / 4] = make_float4(p[0] * inv, p[4] * inv, p[1] * inv, p[5] * inv);
-            dst[8 * c + k / 4 + 1] = make_float4(p[2] * inv, p[6] * inv, p[3] * inv, p[7] * inv);
-          }
+      for (int r = 0; r < 2; ++r) {
+        float v = sum[r][0] + sum[r][1];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        inv[r] = 1.0f / v;
+        const int row = first + first_row + (lane >> 2) + 8 * r;
+        const int64_t at = part + (row < R ? query_row(0, row, G, a.H, j) : 0);
+        if (row < R && (lane & 3) == 0) part_lse[at] = shift[r] + log2f(v);
+        // lane % 4 = 0 .. 3 writes columns 0, 4, 2, 6 and the one behind of each 8
+        dst[r] = row < R ? part_o + at * kD + 4 * (lane & 1) + (lane & 2) : nullptr;
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float o[32];
+        ld_16x64(to + 64 * g, o);
+        ld_wait32(o);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const int r = (k >> 1) & 1;
+          // this thread has two columns of equal parity, lane ^ 2 their neighbours
+          const float give = (lane & 2) ? o[k] : o[k + 1];
+          const float got = __shfl_xor_sync(0xffffffffu, give, 2);
+          const float2 w = (lane & 2) ? make_float2(got, o[k + 1]) : make_float2(o[k], got);
+          if (dst[r])
+            *reinterpret_cast<float2 *>(dst[r] + 64 * g + 8 * (k >> 2)) =
+                make_float2(w.x * inv[r], w.y * inv[r]);
+        }
       }
       tc_fence_before();
     }
-  } else if (warp < 12) {
-    setmaxnreg_dec<kRegOperand>();
-    const int tid = threadIdx.x - 256, w = warp - 8;
+  } else if (warp < kIssueWarp) {
+    const int tid = threadIdx.x - 32 * kSoftmaxWarps, w = warp - kSoftmaxWarps;
+    const KvPlanes &c = a.prefix;
     int it = 0;
-    bool ok = true;
-    Words kw, vw;
-    bool more = un.next(item, t0, n);
-    if (more)
-      load_words<MODE>(kw, a.prefix.k_hi, a.prefix.k_lo, (int64_t)t0 * kTokens, a.P, Hkv,
-                       item / pl.tc_groups, tid);
-    while (ok && more) {
-      const int j = item / pl.tc_groups;
-      int next_item = item;
-      int next_t0 = t0, next_n = n;
-      for (int i = 0; i < n; ++i, ++it) {
-        const int64_t tok = (int64_t)(t0 + i) * kTokens;
-        const int s = it & (kStages - 1), slot = it & (kSlots - 1);
-        const uint32_t free_parity = ((it / kStages) & 1) ^ 1;
-        load_words<MODE>(vw, a.prefix.v_hi, a.prefix.v_lo, tok, a.P, Hkv, j, tid);
-        float fk = 0.0f, fv = 0.0f;
-        if (tok + tid < a.P) {
-          const int64_t row = (tok + tid) * Hkv + j;
-          fk = half_bits(__ldg(a.prefix.k_scale + row)) * (MODE ? 0.0625f * kScale : kScale);
-          fv = half_bits(__ldg(a.prefix.v_scale + row)) * (MODE ? 0.0625f : 1.0f);
-        }
-        ok = mbar_wait_warp(&k_free[s], free_parity);
-        if (!ok) break;
-        scales[slot * 2 * kTokens + tid] = fk;
-        scales[slot * 2 * kTokens + kTokens + tid] = fv;
-        int e = fv > 0.0f ? (int)((__float_as_uint(fv) >> 23) & 0xFFu) - 126 : kMinExp;
-        e = __reduce_max_sync(0xffffffffu, min(e, 40));
-        if (lane == 0) exps[4 * slot + w] = e;
-        store_words<MODE>(sm + kOffK + s * kOperand, kw, tid);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sc_full[slot]);
-          mbar_arrive(&k_full[s]);
-        }
-        // the next tile's K words while V is written
-        if (i + 1 < n) {
-          load_words<MODE>(kw, a.prefix.k_hi, a.prefix.k_lo, tok + kTokens, a.P, Hkv, j, tid);
-        } else {
-          more = un.next(next_item, next_t0, next_n);
-          if (more)
-            load_words<MODE>(kw, a.prefix.k_hi, a.prefix.k_lo, (int64_t)next_t0 * kTokens, a.P, Hkv,
-                             next_item / pl.tc_groups, tid);
-        }
-        ok = mbar_wait_warp(&v_free[s], free_parity);
-        if (!ok) break;
-        store_words<MODE>(sm + kOffV + s * kOperand, vw, tid);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[s]);
+    bool ok = true, more = un.next(item, t0, n);
+    // K words and scales are loaded while the V before is written, V words
+    // while K is: 64 words at a time in registers
+    Words kv;
+    uint16_t sk = 0, sv = 0;
+    auto load_scales = [&](int64_t tok, int j) {
+      sk = sv = 0;
+      if (tok + tid < a.P) {
+        sk = __ldg(c.k_scale + (tok + tid) * Hkv + j);
+        sv = __ldg(c.v_scale + (tok + tid) * Hkv + j);
       }
-      item = next_item;
-      t0 = next_t0;
-      n = next_n;
+    };
+    if (more) {
+      const int j = item / pl.tc_groups;
+      const Rows r = rows_of((int64_t)t0 * kTokens, Hkv, j, tid);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) load_words<MODE>(kv, q, c.k_hi, c.k_lo, r, a.P, Hkv);
+      load_scales((int64_t)t0 * kTokens, j);
+    }
+    while (ok && more) {
+      const int64_t tok = (int64_t)t0 * kTokens;
+      const int s = it & (kStages - 1), slot = it & (kSlots - 1);
+      const uint32_t free_parity = ((it / kStages) & 1) ^ 1;
+      const Rows rv = rows_of(tok, Hkv, item / pl.tc_groups, tid);
+      ok = wait_warp(&k_free[s], free_parity);
+      if (!ok) break;
+      const bool in = tok + tid < a.P;  // behind the prefix: scales 1 and 0
+      const float fk = in ? half_bits(sk) * (MODE ? 0.0625f * kScale : kScale) : 1.0f;
+      const float fv = half_bits(sv) * (MODE ? 0.0625f : 1.0f);
+      const int sc = slot * 2 * kScaleSet + ((tid >> 1) & 3) * kScaleRow + 2 * (tid >> 3) + (tid & 1);
+      scales[sc] = fk;
+      scales[sc + kScaleSet] = fv;
+      int e = fv > 0.0f ? (int)((__float_as_uint(fv) >> 23) & 0xFFu) - 126 : kMinExp;
+      e = __reduce_max_sync(0xffffffffu, min(e, 40));
+      if (lane == 0) exps[4 * slot + w] = e;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        store_words<MODE>(sm + kOffK + s * kOperand, kv, q, tid);
+        load_words<MODE>(kv, q, c.v_hi, c.v_lo, rv, a.P, Hkv);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sc_full[slot]);
+        mbar_arrive(&k_full[s]);
+      }
+      // the next tile
+      ++t0;
+      if (--n == 0) more = un.next(item, t0, n);
+      const int j = item / pl.tc_groups;
+      const Rows rk = rows_of((int64_t)t0 * kTokens, Hkv, j, tid);
+      ok = wait_warp(&v_free[s], free_parity);
+      if (!ok) break;
+      if (more) load_scales((int64_t)t0 * kTokens, j);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        store_words<MODE>(sm + kOffV + s * kOperand, kv, q, tid);
+        if (more) load_words<MODE>(kv, q, c.k_hi, c.k_lo, rk, a.P, Hkv);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[s]);
+      ++it;
     }
   } else {
-    setmaxnreg_dec<kRegIssue>();
-    if (warp == 12 && lane == 0) {
+    {
       const uint64_t qd = umma_desc_sw128(sm + kOffQ), kd = umma_desc_sw128(sm + kOffK),
                      vd = desc_mn_sw128(sm + kOffV);
       constexpr uint64_t kOp = kOperand >> 4;  // descriptor address unit: 16 bytes
       int it = 0, seg = 0, seg_b = 0, sx[2] = {0, 0};
       bool ok = true, issued = false;
+      // The whole warp runs along and one elected thread issues.
       auto scores = [&](int x, int s) {  // S_x = Q_x K^T: 8 k-steps of 16 columns
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t step = (k >> 2) * (kOp / 2) + 2 * (k & 3);
-          mma_ss(tmem + kColS + 128 * x, qd + x * kOp + step, kd + s * kOp + step, idesc(false),
-                 k > 0);
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t step = (k >> 2) * (kOp / 2) + 2 * (k & 3);
+            mma_ss(tmem + kColS + 128 * x, qd + x * kOp + step, kd + s * kOp + step, idesc(false),
+                   k > 0);
+          }
+          umma_commit(&s_full[x]);
         }
-        umma_commit(&s_full[x]);
+        __syncwarp();
         issued = true;
       };
       auto output = [&](int x, int s, bool add) {  // O_x += P_x V: 8 k-steps of 16 tokens
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * k,
-                 vd + s * kOp + (2048 >> 4) * k, idesc(true), add || k > 0);
-        umma_commit(&o_done[x]);
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * k,
+                   vd + s * kOp + (2048 >> 4) * k, idesc(true), add || k > 0);
+          umma_commit(&o_done[x]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t *bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
       };
       while (ok && un.next(item, t0, n)) {
         const bool two = (item % pl.tc_groups) * kRowsCta + kRowsTile < R;
-        ok = mbar_wait(&q_full[0], seg & 1) && (!two || mbar_wait(&q_full[1], seg_b & 1)) &&
-             mbar_wait(&k_full[it & 1], (it >> 1) & 1);
+        ok = wait_warp(&q_full[0], seg & 1) && (!two || wait_warp(&q_full[1], seg_b & 1)) &&
+             wait_warp(&k_full[it & 1], (it >> 1) & 1);
         if (!ok) break;
         ++seg;
         seg_b += two;
         tc_fence_after();
         scores(0, it & 1);
         if (two) scores(1, it & 1);
-        umma_commit(&k_free[it & 1]);
+        commit(&k_free[it & 1]);
         for (int i = 0; i < n; ++i, ++it) {
           const int s = it & 1, s2 = (it + 1) & 1;
           const uint32_t ph = (it >> 1) & 1, ph2 = ((it + 1) >> 1) & 1;
           const bool last = i + 1 == n;
-          ok = mbar_wait(&v_full[s], ph) && mbar_wait(&p_full[0], sx[0] & 1);
+          ok = wait_warp(&v_full[s], ph) && wait_warp(&p_full[0], sx[0] & 1);
           if (!ok) break;
           tc_fence_after();
           output(0, s, i > 0);
           ++sx[0];
           if (!last) {
-            ok = mbar_wait(&k_full[s2], ph2);
+            ok = wait_warp(&k_full[s2], ph2);
             if (!ok) break;
             tc_fence_after();
             scores(0, s2);
           }
           if (two) {
-            ok = mbar_wait(&p_full[1], sx[1] & 1);
+            ok = wait_warp(&p_full[1], sx[1] & 1);
             if (!ok) break;
             tc_fence_after();
             output(1, s, i > 0);
             ++sx[1];
           }
-          umma_commit(&v_free[s]);
+          commit(&v_free[s]);
           if (!last) {
             if (two) scores(1, s2);
-            umma_commit(&k_free[s2]);
+            commit(&k_free[s2]);
           }
         }
       }
       // what was issued must end before tensor memory and the barriers go
       if (issued) {
-        umma_commit(last_done);
+        commit(last_done);
         mbar_wait_final(last_done, 0);
       }
     }
@@ -527,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -535,12 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
 cudaError_t launch_prefix_tc(const PrefixAttnArgs &a, const Plan &p, float *part_lse,
                              float *part_o, cudaStream_t st) {
   auto kern = a.mode ? prefix_tc_kernel<1> : prefix_tc_kernel<0>;
-  // the register split hands out the launch allocation: not launched otherwise
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)p.tc_ctas), dim3(kThreads), kSmem, st, true, a, p,
                     part_lse, part_o);

@@ -31,7 +31,10 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbitnest.so")
 
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+
 _lib = None
+_binding = None
 
 
 class BitnestError(RuntimeError):
@@ -388,45 +391,24 @@ class _KvCacheC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_hi", "k_lo", "k_scale", "v_hi", "v_lo", "v_scale")]
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _serving():
+    """The calls below on tensors (_binding.so, built in-tree by build.py)."""
+    global _binding
+    if _binding is None:
+        import importlib.util
 
+        import torch  # noqa: F401  (its libraries, which the binding uses)
 
-def _run(t, name: str, *args) -> None:
-    """Call an entry point on t's device and its current stream."""
-    import torch
-
-    fn = getattr(lib(), name)
-    if t.device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
-    else:
-        with torch.cuda.device(t.device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(status, name)
-
-
-def _array(t, dtype, shape, device, what: str):
-    """t's address, after checking that it is a contiguous `dtype` array of `shape` there."""
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.device == device
-          and t.is_contiguous(), f"{what}: a contiguous {dtype} array {tuple(shape)} on {device}")
-    return t.data_ptr()
-
-
-def _planes(planes, shape, device, what: str, lo: bool = True):
-    """The addresses of (hi, lo, scale) of the rows `shape`."""
-    import torch
-
-    hi, lo_t, sc = planes
-    half = (*shape, GROUP // 2)
-    return (_array(hi, torch.uint8, half, device, what + " hi"),
-            _array(lo_t, torch.uint8, half, device, what + " lo") if lo else None,
-            _array(sc, torch.float16, shape, device, what + " scale"))
-
-
-def _cache(k_planes, v_planes, shape, device, what: str, lo: bool = True):
-    return _KvCacheC(*_planes(k_planes, shape, device, what + " k", lo),
-                     *_planes(v_planes, shape, device, what + " v", lo))
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(
+                f"{BINDING_PATH} is missing: build it with `python -m w8_quantized_linear_b200.build`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.open(tuple(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in m.names),
+               BitnestError)
+        _binding = m
+    return _binding
 
 
 def nested_cache(cap: int, Hkv: int, batch: int | None = None, device="cuda"):
@@ -460,23 +442,7 @@ def rope(x, pos, phases, magnitude: float = 1.0, layout: int = ROPE_HALF, invers
     or fp32 [M, heads, D] (any strides of tokens and heads), pos int32 [M].
     `out` (which may be x) or a new contiguous array of `dtype` (default fp16).
     `inverse` turns back: the gradient of x from out's."""
-    import torch
-
-    M, heads, D = x.shape
-    types = {torch.float16: 0, torch.float32: 1}
-    y = out if out is not None else torch.empty((M, heads, D), dtype=dtype or torch.float16,
-                                                device=x.device)
-    _need(x.dtype in types and y.dtype in types, "rope: fp16 or fp32 arrays")
-    _need(x.is_cuda and y.device == x.device and y.shape == x.shape, "rope: out like x, on a GPU")
-    xs, ys = x.stride(), y.stride()
-    _need((xs[2] == 1 and ys[2] == 1) or x.numel() == 0, "rope: a head's values lie together")
-    _need(phases.dim() == 1, "rope: phases [rot / 2]")
-    _run(x, "bitnest_rope", x.data_ptr(), types[x.dtype], xs[0], xs[1],
-         _array(pos, torch.int32, (M,), x.device, "rope: pos"),
-         _array(phases, torch.int64, phases.shape, x.device, "rope: phases"), float(magnitude), M,
-         heads, D, 2 * phases.numel(), int(layout), int(inverse), y.data_ptr(), types[y.dtype],
-         ys[0], ys[1])
-    return y
+    return _serving().rope(x, pos, phases, magnitude, layout, inverse, out, dtype)
 
 
 def kv_append(k, v, start, k_planes, v_planes, pos=None, phases=None, magnitude: float = 1.0,
@@ -485,53 +451,14 @@ def kv_append(k, v, start, k_planes, v_planes, pos=None, phases=None, magnitude:
     nested cache [B, cap, Hkv]: token i of sequence b becomes row start[b] + i,
     where i < count[b] if given.  With `phases` the keys are turned by pos
     int32 [B, L] first (see rope)."""
-    import torch
-
-    B, L, Hkv, D = k.shape
-    types = {torch.float16: 0, torch.float32: 1}
-    _need(k.dtype in types and v.dtype == k.dtype, "kv_append: fp16 or fp32 k and v")
-    _need(k.is_cuda and v.device == k.device and v.shape == k.shape and D == GROUP,
-          "kv_append: k and v [B, L, Hkv, 128] on a GPU")
-    strides = []
-    for t in (k, v):
-        s = t.stride()
-        step = s[1] if L > 1 else s[0] if B > 1 else Hkv * D
-        _need(t.numel() == 0 or (s[3] == 1 and (s[2] == D or Hkv == 1)
-                                 and (B == 1 or s[0] == L * step)),
-              "kv_append: a token's heads lie together, tokens at one stride")
-        strides.append(step)
-    cap = k_planes[0].shape[1]
-    cache = _cache(k_planes, v_planes, (B, cap, Hkv), k.device, "kv_append:")
-    dev = k.device
-    rot = 0
-    if phases is not None:
-        _need(pos is not None and phases.dim() == 1, "kv_append: pos and phases [rot / 2]")
-        rot = 2 * phases.numel()
-    _run(k, "bitnest_kv_append", k.data_ptr(), strides[0], v.data_ptr(), strides[1],
-         types[k.dtype], B, L, Hkv, _array(start, torch.int32, (B,), dev, "kv_append: start"),
-         None if count is None else _array(count, torch.int32, (B,), dev, "kv_append: count"),
-         None if phases is None else _array(pos, torch.int32, (B, L), dev, "kv_append: pos"),
-         None if phases is None else _array(phases, torch.int64, phases.shape, dev,
-                                            "kv_append: phases"),
-         float(magnitude), rot, int(layout), ctypes.byref(cache), cap)
+    _serving().kv_append(k, v, start, k_planes, v_planes, pos, phases, magnitude, layout, count)
 
 
 def kv_read(mode: int, start, L: int, k_planes, v_planes):
     """(k, v) fp16 [B, L, Hkv, 128]: the draft's or target's values of rows
     start[b] .. start[b] + L - 1 (start None: 0) of a nested cache; rows
     outside the cache read as zeros."""
-    import torch
-
-    B, cap, Hkv, _ = k_planes[0].shape
-    dev = k_planes[0].device
-    _need(dev.type == "cuda" and L >= 0, "kv_read: L rows of a cache on a GPU")
-    cache = _cache(k_planes, v_planes, (B, cap, Hkv), dev, "kv_read:", lo=mode != DRAFT)
-    k = torch.empty((B, L, Hkv, GROUP), dtype=torch.float16, device=dev)
-    v = torch.empty_like(k)
-    _run(k, "bitnest_kv_read", int(mode), ctypes.byref(cache), B, cap, Hkv,
-         None if start is None else _array(start, torch.int32, (B,), dev, "kv_read: start"),
-         int(L), k.data_ptr(), v.data_ptr())
-    return k, v
+    return _serving().kv_read(mode, start, L, k_planes, v_planes)
 
 
 def prefix_attention_ws_bytes(B: int, L: int, H: int, Hkv: int, P: int, cap: int) -> int:
@@ -550,34 +477,7 @@ def prefix_attention(mode: int, q, prefix, own, lens, out=None, lse=None, ws=Non
     [B].  Query i of sequence b sees the prefix and own tokens
     t <= lens[b] - L + i.  Returns (out fp16 [B, L, H, 128], lse fp32 [B, L, H]).
     `ws`: scratch of prefix_attention_ws_bytes bytes (uint8), else taken here."""
-    import torch
-
-    B, L, H, D = q.shape
-    dev = q.device
-    _need(q.is_cuda and D == GROUP, "prefix_attention: q fp16 [B, L, H, 128] on a GPU")
-    _need(prefix is not None or own is not None, "prefix_attention: a prefix or own tokens")
-    lo = mode != DRAFT
-    P = cap = 0
-    if own is not None:
-        cap, Hkv = own[0][0].shape[1:3]
-    if prefix is not None:
-        P, Hkv = prefix[0][0].shape[:2]
-    pc = None if P == 0 else ctypes.byref(_cache(*prefix, (P, Hkv), dev, "prefix_attention: prefix", lo))
-    oc = None if cap == 0 else ctypes.byref(_cache(*own, (B, cap, Hkv), dev, "prefix_attention: own", lo))
-    o = out if out is not None else torch.empty((B, L, H, D), dtype=torch.float16, device=dev)
-    e = lse if lse is not None else torch.empty((B, L, H), dtype=torch.float32, device=dev)
-    if ws is None:
-        n = prefix_attention_ws_bytes(B, L, H, Hkv, P, cap)
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    _need(ws.dtype == torch.uint8 and ws.device == dev and ws.is_contiguous(),
-          "prefix_attention: ws, bytes on q's device")
-    _run(q, "bitnest_prefix_attention", int(mode),
-         _array(q, torch.float16, q.shape, dev, "prefix_attention: q"), B, L, H, Hkv, D, pc, P, oc,
-         cap, _array(lens, torch.int32, (B,), dev, "prefix_attention: lens"),
-         _array(o, torch.float16, q.shape, dev, "prefix_attention: out"),
-         _array(e, torch.float32, (B, L, H), dev, "prefix_attention: lse"), ws.data_ptr(),
-         ws.numel())
-    return o, e
+    return _serving().prefix_attention(mode, q, prefix, own, lens, out, lse, ws)
 
 
 def kv_weights(mode: int, q, lse, k_planes, acc, lens=None):
@@ -585,22 +485,7 @@ def kv_weights(mode: int, q, lse, k_planes, acc, lens=None):
     prefix_attention's lse) to acc: with lens each sequence's own cache, planes
     [B, cap, Hkv, ..] and acc fp32 [B, Hkv, cap]; without, one prefix that all
     see, planes [P, Hkv, ..] and acc fp32 [Hkv, P].  Returns acc."""
-    import torch
-
-    B, L, H, D = q.shape
-    dev = q.device
-    _need(q.is_cuda and D == GROUP, "kv_weights: q fp16 [B, L, H, 128] on a GPU")
-    hi = k_planes[0]
-    _need(hi.dim() == (3 if lens is None else 4), "kv_weights: planes [B, cap, Hkv, 64] with lens, "
-          "[P, Hkv, 64] without")
-    cap, Hkv = hi.shape[-3:-1]
-    rows, sums = ((cap, Hkv), (Hkv, cap)) if lens is None else ((B, cap, Hkv), (B, Hkv, cap))
-    p = _planes(k_planes, rows, dev, "kv_weights: k", lo=mode != DRAFT)
-    _run(q, "bitnest_kv_weights", int(mode), _array(q, torch.float16, q.shape, dev, "kv_weights: q"),
-         _array(lse, torch.float32, (B, L, H), dev, "kv_weights: lse"), B, L, H, Hkv, D, *p, cap,
-         None if lens is None else _array(lens, torch.int32, (B,), dev, "kv_weights: lens"),
-         _array(acc, torch.float32, sums, dev, "kv_weights: acc"))
-    return acc
+    return _serving().kv_weights(mode, q, lse, k_planes, acc, lens)
 
 
 def kv_evict(acc, lens, keep: int, sinks: int, recent: int, k_planes, v_planes, k_out, v_out,
@@ -609,20 +494,5 @@ def kv_evict(acc, lens, keep: int, sinks: int, recent: int, k_planes, v_planes, 
     `keep` tokens in all, of every sequence and KV head of a nested cache; they
     and their acc go to another cache (k_out, v_out, acc_out [B, Hkv, cap_out]).
     Returns (kept int32 [B, Hkv, keep], -1 behind the last; lens int32 [B])."""
-    import torch
-
-    hi = k_planes[0]
-    dev = hi.device
-    B, cap, Hkv, _ = hi.shape
-    cap_out = k_out[0].shape[1]
-    _need(dev.type == "cuda", "kv_evict: a cache on a GPU")
-    src = _cache(k_planes, v_planes, (B, cap, Hkv), dev, "kv_evict:")
-    dst = _cache(k_out, v_out, (B, cap_out, Hkv), dev, "kv_evict: out")
-    kept = torch.empty((B, Hkv, max(int(keep), 0)), dtype=torch.int32, device=dev)
-    n = torch.empty(B, dtype=torch.int32, device=dev)
-    _run(hi, "bitnest_kv_evict", _array(acc, torch.float32, (B, Hkv, cap), dev, "kv_evict: acc"),
-         _array(lens, torch.int32, (B,), dev, "kv_evict: lens"), B, Hkv, cap, int(keep),
-         int(sinks), int(recent), ctypes.byref(src), ctypes.byref(dst), cap_out,
-         _array(acc_out, torch.float32, (B, Hkv, cap_out), dev, "kv_evict: acc_out"),
-         kept.data_ptr(), n.data_ptr())
-    return kept, n
+    return _serving().kv_evict(acc, lens, keep, sinks, recent, k_planes, v_planes, k_out, v_out,
+                               acc_out)

@@ -1,16 +1,21 @@
-"""Build the sm_100a shared library libbitnest.so in-tree with nvcc."""
+"""Build the sm_100a shared library libbitnest.so in-tree with nvcc, and the
+package's binding of the serving calls to torch tensors (_binding.so) with g++."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libbitnest.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -33,7 +38,31 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/torch_binding.cpp against the torch that is installed (its
+    headers and host libraries; it loads them, and the CUDA library, itself)."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "bitnest.h")]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [INCLUDE, os.path.join(torch, "include"),
+           os.path.join(torch, "include/torch/csrc/api/include"), os.path.join(cuda, "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", *("-I" + d for d in inc), BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -84,17 +84,18 @@ const char *bitnest_status_string(int status) {
 int bitnest_version(void) { return 100; }
 
 int bitnest_device_wait_timeout(int reset) {
-  int f1 = 0, f2 = 0, f3 = 0;
+  int f1 = 0, f2 = 0, f3 = 0, f4 = 0;
   if (read_wait_timeout(&f1, reset != 0) != cudaSuccess) return -BITNEST_ERR_CUDA;
   if (read_wait_timeout_gemv(&f2, reset != 0) != cudaSuccess) return -BITNEST_ERR_CUDA;
   if (read_wait_timeout_prefix(&f3, reset != 0) != cudaSuccess) return -BITNEST_ERR_CUDA;
+  if (read_wait_timeout_weights(&f4, reset != 0) != cudaSuccess) return -BITNEST_ERR_CUDA;
   // a split call that gave up may have left arrivals in the counters of the
   // library's static scratch: the reset clears them as well
   if (reset && f1) {
     if (tc_static_ws_clear_counters(nullptr) != cudaSuccess) return -BITNEST_ERR_CUDA;
     if (cudaDeviceSynchronize() != cudaSuccess) return -BITNEST_ERR_CUDA;
   }
-  return (f1 | f2 | f3) ? 1 : 0;
+  return (f1 | f2 | f3 | f4) ? 1 : 0;
 }
 
 int bitnest_debug_wait_probe(void *stream) {

@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(256) gather_kernel(KvEvictArgs a, int runs) {
 cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st) {
   const int G = (int)(a.H / a.Hkv);
   const int64_t R = (a.len ? a.L : a.B * a.L) * G;
+  if (!a.len && R >= 128) return evict::launch_weights_tc(a, st);
   // The warps of a CTA share the rows of its tokens when there are more rows
   // than a warp's pass and too few tokens to give every warp its own.
   const int64_t caches = (a.len ? a.B : 1) * a.Hkv;

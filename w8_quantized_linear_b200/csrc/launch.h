@@ -122,6 +122,10 @@ struct KvWeightsArgs {
   float *acc;
 };
 cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st);
+namespace evict {
+cudaError_t launch_weights_tc(const KvWeightsArgs &a, cudaStream_t st);  // len null
+}
+cudaError_t read_wait_timeout_weights(int *flag, bool reset);
 
 struct KvEvictArgs {
   const float *acc;  // [B, Hkv, cap]

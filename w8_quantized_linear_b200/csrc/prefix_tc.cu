@@ -32,6 +32,7 @@
 #include "nested_mma.cuh"
 #include "prefix_plan.h"
 #include "sm100.cuh"
+#include "tc_f16.cuh"
 
 namespace bitnest {
 namespace pattn {
@@ -39,6 +40,7 @@ namespace pattn {
 namespace {
 
 using namespace nested;
+using namespace tc16;
 
 constexpr int kRowsTile = 128, kRowsCta = 256, kTokens = 128;
 constexpr int kSoftmaxWarps = 16, kOperandWarps = 4;
@@ -65,31 +67,6 @@ constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 
 constexpr int kColO = 0, kColS = 256;  // tensor memory columns (tile B: + 128)
 
-// kind::f16 with fp32 accumulation: A fp16 (K-major), B fp16 (K-major, or
-// MN-major when bn), 128 x 128
-constexpr uint32_t idesc(bool bn) {
-  return (1u << 4) | (bn ? 1u << 16 : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-// D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(accumulate)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(accumulate)
-      : "memory");
-}
-
 // MN-major operand, 128-byte swizzle: 64 columns (128 bytes) of one token a
 // line, 8 tokens 1024 bytes, the next 64 columns 16 KB on.
 __device__ __forceinline__ uint64_t desc_mn_sw128(const void *base) {
@@ -100,87 +77,6 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(const void *base) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-// 16 lanes x 64 columns: thread t gets of lane t / 4 the columns 8 n + 2 (t % 4), + 1 in
-// r[4 n], r[4 n + 1], and of lane t / 4 + 8 the same columns in r[4 n + 2], r[4 n + 3].
-__device__ __forceinline__ void ld_16x64(uint32_t taddr, float (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
-      : "r"(taddr));
-}
-// 16 lanes x 8 columns, as above.
-__device__ __forceinline__ void ld_16x8(uint32_t taddr, float (&r)[4]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void st_16x8(uint32_t taddr, const float (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
-               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3])
-               : "memory");
-}
-// 16 lanes x 32 columns: lane t / 4, column 4 n + t % 4 from r[2 n], lane t / 4 + 8 from r[2 n + 1].
-__device__ __forceinline__ void st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// True in one thread of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-// Wait for the loads issued so far; r passes through, so that nothing that uses
-// it can move in front.
-__device__ __forceinline__ void ld_wait32(float (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
-                 "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
-                 "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
-                 "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
-                 "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
-                 "+f"(r[30]), "+f"(r[31])::"memory");
-}
-
-// mbar_wait for waits that are short and frequent: no look at the timer before
-// some hundreds of tries.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0u) {
-      if (*(volatile int *)&g_wait_timeout) return false;
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) break;
-    }
-  }
-  atomicExch(&g_wait_timeout, 1);
-  return false;
-}
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait(bar, parity));
-}
-
-__device__ __forceinline__ void f32x2_fma(float &d0, float &d1, float a0, float a1, float b0,
-                                          float b1, float c0, float c1) {
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

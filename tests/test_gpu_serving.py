@@ -421,6 +421,33 @@ def test_weights_match_oracle(B, L, H, Hkv, cap, lens, mode):
     assert np.all(np.abs(host(d_acc) - want) <= rel * (want - acc) + 2 * U * np.abs(want))
 
 
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("B,L,H,Hkv,P", [
+    (32, 1, 16, 4, 128),       # 128 rows, one row tile; fewer token tiles than SMs
+    (129, 1, 4, 4, 6000),      # 129 rows; 188 token tiles: one or two a CTA, runs across heads
+    (16, 4, 32, 8, 9001),      # 256 rows; 568 token tiles, three or four a CTA
+    (65, 2, 16, 2, 19000),     # 1040 rows; 298 tiles
+    (150, 1, 2, 2, 38000)])    # one head a KV head; 594 tiles, four or five a CTA
+def test_weights_of_many_rows_match_oracle(B, L, H, Hkv, P, mode):
+    """The shared prefix's weights where a KV head has 128 rows or more, over the
+    ways in which token tiles are dealt out; a few rows without weight."""
+    rng = np.random.default_rng(P)
+    q = (rng.standard_normal((B, L, H, 128)) * 1.2).astype(np.float16)
+    k = tuple(rng.integers(0, 256, (P, Hkv, 64)).astype(np.uint8) for _ in range(2)) + (
+        (rng.random((P, Hkv)) * 0.2).astype(np.float16),)
+    lse = (rng.standard_normal((B, L, H)) + 20.0).astype(np.float32)
+    lse[0, 0, 0] = lse[B // 2, 0, H - 1] = lse[B - 1, L - 1, H - 1] = -np.inf
+    acc = rng.random((Hkv, P)).astype(np.float32)
+    want = ref.weights(mode, q, lse, k, acc, None)
+    got = host(bn.kv_weights(mode, dev(q), dev(lse), tuple(dev(x) for x in k), dev(acc)))
+    # as in Attend.bounds and test_weights_match_oracle
+    kv = np.abs(ref.values(mode, k).reshape(-1, 128)).max(0)
+    ds = 2.0 ** -16 * float((np.abs(q.astype(np.float64)).max(axis=(0, 1, 2)) * kv).sum()) / np.sqrt(128)
+    ds += 2.0 ** -21 * (1 + np.abs(lse[np.isfinite(lse)]).max())
+    rel = 2 * ds + 2.0 ** -20 * (1 + np.abs(lse[np.isfinite(lse)]).max()) + (B * L * H // Hkv + 2) * U
+    assert np.all(np.abs(got - want) <= rel * (want - acc) + 2 * U * np.abs(want))
+
+
 def test_weights_of_a_softmax_sum_to_one():
     """Prefix and own weights with the attention's own lse: one for each row."""
     B, L, H, Hkv = 4, 3, 8, 2

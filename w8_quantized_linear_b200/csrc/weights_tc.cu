@@ -5,15 +5,16 @@
 // token's sum stays in one quarter-warp for the whole pass, and nothing is
 // reduced across threads before the end.
 //
-// A CTA takes an equal run of token tiles over all KV heads, up to four at a
-// time, whose codes stay in shared memory while the rows pass by in tiles of
-// 128.  Four slots (128 columns of tensor memory, four warps) work at a time:
-// one for each of four token tiles, or, where there are fewer, on different
-// row tiles of the same one.  21 warps:
-//   0-15   slot warp / 4: codes -> fp16 operand, then the weights of its
-//          products from tensor memory, in pieces of 16 tokens x 64 rows;
-//   16-19  bring the row tiles (TMA) and their lse;
-//   20     issues the MMAs.
+// A CTA takes an equal run of token tiles over all KV heads, two at a time (a
+// segment), whose codes stay in shared memory while the rows pass by in tiles
+// of 128.  Four slots (128 columns of tensor memory, four warps) work at a
+// time, on two row tiles of each of two token tiles, or on four of one.  The
+// next segment's codes are written meanwhile.  22 warps:
+//   0-15   slot warp / 4: the weights of its products from tensor memory, in
+//          pieces of 16 tokens x 64 rows;
+//   16-19  codes -> fp16 operand, and the tokens' scales;
+//   20     issues the MMAs;
+//   21     brings the row tiles (TMA) and their lse.
 //
 // Bound: the exponentials.  16 a cycle and SM make 1024 cycles a product of
 // 128 x 128, its MMAs 512.
@@ -35,22 +36,26 @@ using namespace tc16;
 
 constexpr int kSms = 148;
 constexpr int kTile = 128;
-constexpr int kSlots = 4, kStages = 2, kSets = 8;
-constexpr int kSlotWarps = 4 * kSlots, kLoadWarps = 4, kIssueWarp = kSlotWarps + kLoadWarps;
-constexpr int kThreads = (kIssueWarp + 1) * 32;
+constexpr int kSlots = 4, kPair = 2, kStages = 2, kSets = 8;
+constexpr int kSlotWarps = 4 * kSlots, kCodeWarps = 4;
+constexpr int kIssueWarp = kSlotWarps + kCodeWarps, kRowWarp = kIssueWarp + 1;
+constexpr int kThreads = (kRowWarp + 1) * 32;
 constexpr int kOperand = kTile * kD * 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
 
 // A set: -lse log2(e) of a row tile, row 8 n + 2 q + i at q * kSetRow + 2 n + i, the
-// order in which a thread of lane % 4 = q holds its columns, rows in different banks
+// order in which a thread of lane % 4 = q holds its columns, rows in different banks.
+// Eight of them: a set is read by slots whose products come before the one that frees
+// the stage of the row tile six later, and the loader waits for that.
 constexpr int kSetRow = 36, kSet = 4 * kSetRow;
-constexpr int kOffK = 0;
-constexpr int kOffQ = kOffK + kSlots * kOperand;
+constexpr int kOffK = 0;  // [segment % 2][tile]
+constexpr int kOffQ = kOffK + 2 * kPair * kOperand;
 constexpr int kOffSet = kOffQ + kStages * kOperand;
-constexpr int kOffPart = kOffSet + kSets * kSet * 4;
-constexpr int kOffBar = kOffPart + kSlots * kTile * 4;
-constexpr int kBars = 2 * kStages + kSets + 2 * kSlots + 2;
+constexpr int kOffPart = kOffSet + kSets * kSet * 4;        // [segment % 2][slot][token]
+constexpr int kOffFactor = kOffPart + 2 * kSlots * kTile * 4;  // [segment % 2][tile][token]
+constexpr int kOffBar = kOffFactor + 2 * kPair * kTile * 4;
+constexpr int kBars = 2 * kStages + kSets + 2 * kSlots + 4 + 1;
 constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_t *bar, int x,
@@ -71,7 +76,7 @@ struct Run {  // a CTA's run of tiles
     if (u >= end) return false;
     s.j = u / per_head;
     s.first = u - s.j * per_head;
-    s.nt = min(min(end - u, per_head - s.first), kSlots);
+    s.nt = min(min(end - u, per_head - s.first), kPair);
     s.ways = kSlots / s.nt;
     u += s.nt;
     return true;
@@ -85,10 +90,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);
   float *sets = reinterpret_cast<float *>(sm + kOffSet);
   float *part = reinterpret_cast<float *>(sm + kOffPart);
+  float *factor = reinterpret_cast<float *>(sm + kOffFactor);
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
   uint64_t *q_full = bars, *q_free = q_full + kStages, *set_full = q_free + kStages,
            *s_full = set_full + kSets, *s_free = s_full + kSlots, *k_full = s_free + kSlots,
-           *last_done = k_full + 1;
+           *k_free = k_full + 2, *last_done = k_free + 2;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = (int)a.Hkv, cap = (int)a.cap, R = (int)(a.B * a.L) * G;
@@ -99,12 +105,15 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
       mbar_init(&q_full[s], 1);
       mbar_init(&q_free[s], 1);
     }
-    for (int s = 0; s < kSets; ++s) mbar_init(&set_full[s], kLoadWarps);
+    for (int s = 0; s < kSets; ++s) mbar_init(&set_full[s], 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&s_free[s], 4);
     }
-    mbar_init(k_full, kSlotWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], kCodeWarps);
+      mbar_init(&k_free[s], kSlotWarps + 1);
+    }
     mbar_init(last_done, 1);
     fence_barrier_init();
   }
@@ -131,48 +140,23 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
     const uint32_t ts = tmem + ((uint32_t)(32 * quarter) << 16) + kTile * slot;
     int uses = 0, q0 = 0;  // of this slot; row tiles before this segment
     bool ok = true;
-    while (run.next(sg)) {
-      const int tile = slot % sg.nt, phase = slot / sg.nt;
-      const bool active = phase < sg.ways;
+    for (int seg = 0; run.next(sg); ++seg) {
+      const int tile = slot % sg.nt, phase = slot / sg.nt, buf = seg & 1;
       const int t0 = (sg.first + tile) * kTile;
-      if (phase == 0) {  // the tile's codes: a thread's token
-        const int row = 32 * quarter + lane, t = t0 + row;
-        uint8_t *dst = sm + kOffK + tile * kOperand + row * 128;
-        const int64_t off = ((int64_t)t * Hkv + sg.j) * (kD / 2);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint4 h = make_uint4(0, 0, 0, 0), l = h;
-          if (t < cap) {
-            h = __ldg(reinterpret_cast<const uint4 *>(a.k_hi + off) + p);
-            if (MODE) l = __ldg(reinterpret_cast<const uint4 *>(a.k_lo + off) + p);
-          }
-          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 8 columns
-            uint32_t ev, od;
-            codes<MODE>(hw[c], lw[c], ev, od);
-            const int chunk = 4 * (p & 1) + c;
-            *reinterpret_cast<uint4 *>(dst + (p >> 1) * (kOperand / 2) + ((chunk ^ (row & 7)) << 4)) =
-                make_uint4(pair<MODE>(ev, od, 0), pair<MODE>(ev, od, 1), pair<MODE>(ev, od, 2),
-                           pair<MODE>(ev, od, 3));
-          }
-        }
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(k_full);
-
       // this thread's tokens: lane / 4 + 8 i of the warp's 32
       float f[4], sum[4][2];
+      const int mine = t0 + 32 * quarter + lane;  // and the one whose sum it adds, if phase is 0
+      float *const acc = a.acc + (int64_t)sg.j * cap + mine;
+      const float old = phase == 0 && mine < cap ? *acc : 0.0f;  // early: used at the end
+      ok = ok && wait_warp(&k_full[buf], (seg >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 32 * quarter + 8 * i + (lane >> 2);
-        f[i] = t < cap ? half_bits(__ldg(a.k_scale + (int64_t)t * Hkv + sg.j)) *
-                             (MODE ? 0.0625f * kScale : kScale)
-                       : 0.0f;
+        f[i] = factor[(buf * kPair + tile) * kTile + 32 * quarter + 8 * i + (lane >> 2)];
         sum[i][0] = sum[i][1] = 0.0f;
       }
-      for (int i = phase; active && ok && i < row_tiles; i += sg.ways) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_free[buf]);
+      for (int i = phase; ok && i < row_tiles; i += sg.ways) {
         const int set = (q0 + i) & (kSets - 1);
         const float *b = sets + set * kSet + (lane & 3) * kSetRow;
         ok = wait_warp(&s_full[slot], uses & 1) && wait_warp(&set_full[set], ((q0 + i) / kSets) & 1);
@@ -215,21 +199,65 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
         float v = sum[i][0] + sum[i][1];
         v += __shfl_xor_sync(0xffffffffu, v, 1);
         v += __shfl_xor_sync(0xffffffffu, v, 2);
-        if ((lane & 3) == 0) part[slot * kTile + 32 * quarter + 8 * i + (lane >> 2)] = v;
+        if ((lane & 3) == 0)
+          part[(buf * kSlots + slot) * kTile + 32 * quarter + 8 * i + (lane >> 2)] = v;
       }
-      // every slot is here after the products it used (or a wait that gave up): the
-      // sums are complete, and the operands may be written again
+      // every slot comes here, after a wait that gave up too
       asm volatile("bar.sync 1, %0;" ::"n"(kSlotWarps * 32) : "memory");
-      const int t = t0 + 32 * quarter + lane;
-      if (phase == 0 && ok && t < cap) {
+      if (phase == 0 && ok && mine < cap) {
         float v = 0.0f;
-        for (int w = 0; w < sg.ways; ++w) v += part[(w * sg.nt + tile) * kTile + 32 * quarter + lane];
-        a.acc[(int64_t)sg.j * cap + t] += v;
+        for (int w = 0; w < sg.ways; ++w) v += part[(buf * kSlots + w * sg.nt + tile) * kTile + 32 * quarter + lane];
+        *acc = old + v;
       }
       __syncwarp();
     }
   } else if (warp < kIssueWarp) {
-    const int tid = threadIdx.x - 32 * kSlotWarps;
+    const int row = threadIdx.x - 32 * kSlotWarps;  // a thread's token of a tile
+    bool ok = true;
+    for (int seg = 0; ok && run.next(sg); ++seg) {
+      const int buf = seg & 1;
+      for (int tile = 0; tile < sg.nt; ++tile) {
+        const int t = (sg.first + tile) * kTile + row;
+        uint8_t *dst = sm + kOffK + (buf * kPair + tile) * kOperand + row * 128;
+        const int64_t at = (int64_t)t * Hkv + sg.j, off = at * (kD / 2);
+        uint4 hi[4], lo[4];
+        float f = 0.0f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) hi[p] = lo[p] = make_uint4(0, 0, 0, 0);
+        if (t < cap) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            hi[p] = __ldg(reinterpret_cast<const uint4 *>(a.k_hi + off) + p);
+            if (MODE) lo[p] = __ldg(reinterpret_cast<const uint4 *>(a.k_lo + off) + p);
+          }
+          f = half_bits(__ldg(a.k_scale + at)) * (MODE ? 0.0625f * kScale : kScale);
+        }
+        if (tile == 0) {
+          ok = wait_warp(&k_free[buf], ((seg >> 1) & 1) ^ 1);
+          if (!ok) break;
+        }
+        factor[(buf * kPair + tile) * kTile + row] = f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t hw[4] = {hi[p].x, hi[p].y, hi[p].z, hi[p].w},
+                         lw[4] = {lo[p].x, lo[p].y, lo[p].z, lo[p].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 8 columns
+            uint32_t ev, od;
+            codes<MODE>(hw[c], lw[c], ev, od);
+            const int chunk = 4 * (p & 1) + c;
+            *reinterpret_cast<uint4 *>(dst + (p >> 1) * (kOperand / 2) + ((chunk ^ (row & 7)) << 4)) =
+                make_uint4(pair<MODE>(ev, od, 0), pair<MODE>(ev, od, 1), pair<MODE>(ev, od, 2),
+                           pair<MODE>(ev, od, 3));
+          }
+        }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[buf]);
+    }
+  } else if (warp == kRowWarp) {
     int it = 0;  // row tiles of the CTA
     bool ok = true;
     while (ok && run.next(sg)) {
@@ -237,38 +265,41 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
         const int stage = it & (kStages - 1), set = it & (kSets - 1);
         ok = wait_warp(&q_free[stage], ((it / kStages) & 1) ^ 1);
         if (!ok) break;
-        if (tid == 0) {  // rows of zeros behind the last
+        if (lane == 0) {  // rows of zeros behind the last
           uint8_t *dst = sm + kOffQ + stage * kOperand;
           mbar_arrive_expect_tx(&q_full[stage], kOperand);
           tma_load_3d(dst, &tm_q, &q_full[stage], 0, sg.j * G, i * (kTile / G));
           tma_load_3d(dst + kOperand / 2, &tm_q, &q_full[stage], kD / 2, sg.j * G, i * (kTile / G));
         }
-        const int r = i * kTile + tid;
-        // a row without weight (lse -inf), or behind the last, gives none
-        const float e = r < R ? __ldg(a.lse + query_row(0, r, G, a.H, sg.j)) : -INFINITY;
-        sets[set * kSet + ((tid >> 1) & 3) * kSetRow + 2 * (tid >> 3) + (tid & 1)] =
-            e == -INFINITY ? -INFINITY : -e * kLog2e;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int c = 32 * n + lane, r = i * kTile + c;
+          // a row without weight (lse -inf), or behind the last, gives none
+          const float e = r < R ? __ldg(a.lse + query_row(0, r, G, a.H, sg.j)) : -INFINITY;
+          sets[set * kSet + ((c >> 1) & 3) * kSetRow + 2 * (c >> 3) + (c & 1)] =
+              e == -INFINITY ? -INFINITY : -e * kLog2e;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&set_full[set]);
       }
     }
-    if (!ok && tid == 0)  // gave up: let the copies already issued land
+    if (!ok && lane == 0)  // gave up: let the copies already issued land
       for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
         mbar_wait_final(&q_full[i & (kStages - 1)], (i / kStages) & 1);
     __syncwarp();
   } else {
     const uint64_t kd = umma_desc_sw128(sm + kOffK), qd = umma_desc_sw128(sm + kOffQ);
     constexpr uint64_t kOp = kOperand >> 4;  // descriptor address unit: 16 bytes
-    int it0 = 0, seg = 0, uses[kSlots] = {};
+    int it0 = 0, uses[kSlots] = {};
     bool ok = true, issued = false;
-    while (ok && run.next(sg)) {
-      ok = wait_warp(k_full, seg & 1);
-      ++seg;
+    for (int seg = 0; ok && run.next(sg); ++seg) {
+      const int buf = seg & 1;
+      ok = wait_warp(&k_full[buf], (seg >> 1) & 1);
       for (int i0 = 0; ok && i0 < row_tiles; i0 += sg.ways) {
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) {
           const int phase = s / sg.nt, tile = s - phase * sg.nt, i = i0 + phase;
-          if (!ok || phase >= sg.ways || i >= row_tiles) continue;
+          if (!ok || i >= row_tiles) continue;
           const int stage = (it0 + i) & (kStages - 1);
           if (tile == 0) ok = wait_warp(&q_full[stage], ((it0 + i) / kStages) & 1);
           ok = ok && wait_warp(&s_free[s], (uses[s] & 1) ^ 1);
@@ -279,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint64_t step = (k >> 2) * (kOp / 2) + 2 * (k & 3);
-              mma_ss(tmem + kTile * s, kd + tile * kOp + step, qd + stage * kOp + step,
-                     idesc(false), k > 0);
+              mma_ss(tmem + kTile * s, kd + (buf * kPair + tile) * kOp + step,
+                     qd + stage * kOp + step, idesc(false), k > 0);
             }
             umma_commit(&s_full[s]);
             if (tile == sg.nt - 1) umma_commit(&q_free[stage]);
@@ -288,6 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
           __syncwarp();
           issued = true;
         }
+      }
+      if (ok) {
+        if (elect_one()) umma_commit(&k_free[buf]);
+        __syncwarp();
       }
       it0 += row_tiles;
     }

@@ -12,6 +12,7 @@
 #include "launch.h"
 #include "nested_mma.cuh"
 #include "prefix_plan.h"
+#include "sm100.cuh"
 
 namespace bitnest {
 
@@ -27,66 +28,87 @@ constexpr int kMinExp = -40;  // below any fp16 scale / 16
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
 
-struct Smem {
+// Shared memory of a CTA: the rows' queries as A fragments (4 KB a row tile),
+// then each warp's ring of token tiles; the ring's place holds the warps'
+// states when they join.
+constexpr int kStages = 3;
+constexpr int kFrag = 8 * 32 * 16;                          // a row tile's queries
+__host__ __device__ constexpr int stage_bytes(int mode) { return (mode ? 4 : 2) * kTile * (kD / 2); }
+struct State {
   float m[kWarps][kRows], l[kWarps][kRows];
-  float o[kWarps][kRows][kD];
+  float4 o[kWarps][8][2][32];  // as a lane holds it: [columns tile][rows tile][lane]
 };
-
-struct TileRegs {
-  uint4 kh[2], kl[2];
-  uint2 vh[4], vl[4];
-  uint16_t ks[4], vs[4];
-};
-
-// One tile's loads for one lane (gid = lane / 4, tig = lane % 4): K rows of
-// tokens gid and 8 + gid (16 bytes of each plane at byte 16 tig), V rows of
-// tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9 (8 bytes at byte 8 gid), and
-// the scales of those four tokens.  Tokens at or past t_end read zeros.
-template <int MODE>
-__device__ __forceinline__ void load_tile(TileRegs &r, int t0, int t_end, int64_t row_base, int Hkv,
-                                          int gid, int tig, const KvPlanes &c) {
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int t = t0 + 8 * n + gid;
-    r.kh[n] = r.kl[n] = make_uint4(0, 0, 0, 0);
-    if (t < t_end) {
-      const int64_t off = (row_base + (int64_t)t * Hkv) * (kD / 2) + 16 * tig;
-      r.kh[n] = __ldg(reinterpret_cast<const uint4 *>(c.k_hi + off));
-      if (MODE) r.kl[n] = __ldg(reinterpret_cast<const uint4 *>(c.k_lo + off));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
-    r.vh[i] = r.vl[i] = make_uint2(0, 0);
-    r.ks[i] = r.vs[i] = 0;
-    if (t < t_end) {
-      const int64_t row = row_base + (int64_t)t * Hkv;
-      const int64_t off = row * (kD / 2) + 8 * gid;
-      r.vh[i] = __ldg(reinterpret_cast<const uint2 *>(c.v_hi + off));
-      if (MODE) r.vl[i] = __ldg(reinterpret_cast<const uint2 *>(c.v_lo + off));
-      r.ks[i] = __ldg(c.k_scale + row);
-      r.vs[i] = __ldg(c.v_scale + row);
-    }
-  }
+constexpr int smem_bytes(int mode, int row_tiles) {
+  const int ring = kWarps * kStages * stage_bytes(mode);
+  return row_tiles * kFrag + (ring > (int)sizeof(State) ? ring : (int)sizeof(State));
 }
 
-// One part for a tile of 16 rows: tokens t_begin + 16 (first + n step) .. of
-// the rows' cache, row r seeing tokens below lim(r).  The state goes to slot
-// `warp` of the shared memory.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+
+// One tile's copies for one lane: of each plane the 16-byte pieces of rows
+// lane / 4 and 8 + lane / 4.  A row's pieces lie together; V's are exchanged so
+// that the lanes that read a column's 8 bytes of four row pairs find them in
+// different banks.  The scale of K (lanes 0 to 15) or V (16 to 31) of token
+// lane % 16 is returned.  Tokens at or past t_end are zeros.
 template <int MODE>
-__device__ __forceinline__ void attend(Smem &sh, int warp, int lane, const KvPlanes &c,
-                                       int64_t row_base, int Hkv, int t_begin, int t_end,
-                                       int first, int step, const uint16_t *q0, const uint16_t *q1,
-                                       int lim0, int lim1) {
+__device__ __forceinline__ uint16_t load_tile(uint32_t stage, int t0, int t_end, int64_t row_base,
+                                              int Hkv, int lane, const KvPlanes &c) {
+  constexpr int kPlane = kTile * (kD / 2);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const int r = 8 * n + (lane >> 2), p = lane & 3, t = t0 + r;
+    const bool in = t < t_end;
+    const int64_t off = in ? (row_base + (int64_t)t * Hkv) * (kD / 2) + 16 * p : 0;
+    const uint32_t kd = stage + r * (kD / 2) + 16 * p;
+    const uint32_t vd = stage + (MODE ? 2 : 1) * kPlane + (r >> 1) * kD +
+                        16 * ((((r & 1) << 2) | p) ^ (((r >> 1) & 3) << 1));
+    cp_async16(kd, c.k_hi + off, in);
+    if (MODE) cp_async16(kd + kPlane, c.k_lo + off, in);
+    cp_async16(vd, c.v_hi + off, in);
+    if (MODE) cp_async16(vd + kPlane, c.v_lo + off, in);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  const int t = t0 + (lane & 15);
+  return t < t_end ? __ldg((lane < 16 ? c.k_scale : c.v_scale) + row_base + (int64_t)t * Hkv)
+                   : (uint16_t)0;
+}
+
+// One part for a tile of 16 rows (queries at `frag`): tokens t_begin +
+// 16 (first + n step) .. of the rows' cache, row r seeing tokens below lim(r).
+// The state is left in the registers' layout for store_state.
+struct Part {
+  float m_run[2], l_run[2];
+  float o[8][2][4];  // O^T: columns tile mt, rows tile nt
+  int e_run;         // o holds the output in units of 2^(e_run - 15)
+};
+template <int MODE>
+__device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t ring, int lane,
+                                       const KvPlanes &c, int64_t row_base, int Hkv, int t_begin,
+                                       int t_end, int first, int step, int lim0, int lim1) {
+  constexpr int kPlane = kTile * (kD / 2);
   const int gid = lane >> 2, tig = lane & 3;
   lim0 = min(lim0, t_end);
   lim1 = min(lim1, t_end);
-  uint32_t qa[8][4];
-  load_queries(qa, q0, q1, tig);
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};  // rows gid, gid + 8
-  int e_run = kMinExp;             // o holds the output in units of 2^(e_run - 15)
-  float o[8][2][4];                // O^T: columns tile mt, rows tile nt
+  float(&m_run)[2] = st.m_run, (&l_run)[2] = st.l_run;  // rows gid, gid + 8
+  float(&o)[8][2][4] = st.o;
+  int &e_run = st.e_run;
+  m_run[0] = m_run[1] = -INFINITY;
+  l_run[0] = l_run[1] = 0.0f;
+  e_run = kMinExp;
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -94,40 +116,68 @@ __device__ __forceinline__ void attend(Smem &sh, int warp, int lane, const KvPla
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
-  for (int t0 = t_begin + first * kTile; t0 < t_end; t0 += step * kTile) {
-    TileRegs cur;
-    load_tile<MODE>(cur, t0, t_end, row_base, Hkv, gid, tig, c);
-    float s[2][4];  // [row][token 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig]
+  const int stride = step * kTile;
+  int t0 = t_begin + first * kTile;
+  uint16_t sc[kStages];  // of the tiles in the ring, the oldest first
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint32_t hw[4] = {cur.kh[n].x, cur.kh[n].y, cur.kh[n].z, cur.kh[n].w};
-      const uint32_t lw[4] = {cur.kl[n].x, cur.kl[n].y, cur.kl[n].z, cur.kl[n].w};
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i + 1 < kStages; ++i)
+    sc[i] = load_tile<MODE>(ring + i * stage_bytes(MODE), t0 + i * stride, t_end, row_base, Hkv, lane, c);
+  for (int slot = 0; t0 < t_end; t0 += stride) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // this tile is here, and every lane is done with the one before
+    const int free = slot == 0 ? kStages - 1 : slot - 1;
+    sc[kStages - 1] = load_tile<MODE>(ring + free * stage_bytes(MODE), t0 + (kStages - 1) * stride,
+                                      t_end, row_base, Hkv, lane, c);
+    const uint32_t cur = ring + slot * stage_bytes(MODE);
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    uint16_t ks[4], vs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 2 * tig + (i & 1) + 8 * (i >> 1);
+      ks[i] = (uint16_t)__shfl_sync(0xffffffffu, (int)sc[0], t);
+      vs[i] = (uint16_t)__shfl_sync(0xffffffffu, (int)sc[0], 16 + t);
+    }
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) sc[i] = sc[i + 1];
+    float s[2][4];  // [row][token 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig]
+    {
+      uint4 kh[2], kl[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        kh[n] = lds128(cur + (8 * n + gid) * (kD / 2) + 16 * tig);
+        kl[n] = MODE ? lds128(cur + kPlane + (8 * n + gid) * (kD / 2) + 16 * tig) : make_uint4(0, 0, 0, 0);
+      }
+      float d[2][4] = {};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t ev, od;
-        codes<MODE>(hw[w], lw[w], ev, od);
+        const uint4 q0 = frag[(2 * w) * 32 + lane], q1 = frag[(2 * w + 1) * 32 + lane];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ks = 2 * w + h;
-          mma_f16(d, qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], pair<MODE>(ev, od, 2 * h),
-                  pair<MODE>(ev, od, 2 * h + 1));
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t hw[4] = {kh[n].x, kh[n].y, kh[n].z, kh[n].w};
+          const uint32_t lw[4] = {kl[n].x, kl[n].y, kl[n].z, kl[n].w};
+          uint32_t ev, od;
+          codes<MODE>(hw[w], lw[w], ev, od);
+          mma_f16(d[n], q0.x, q0.y, q0.z, q0.w, pair<MODE>(ev, od, 0), pair<MODE>(ev, od, 1));
+          mma_f16(d[n], q1.x, q1.y, q1.z, q1.w, pair<MODE>(ev, od, 2), pair<MODE>(ev, od, 3));
         }
       }
-      s[0][2 * n] = d[0];
-      s[0][2 * n + 1] = d[1];
-      s[1][2 * n] = d[2];
-      s[1][2 * n + 1] = d[3];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[0][2 * n] = d[n][0];
+        s[0][2 * n + 1] = d[n][1];
+        s[1][2 * n] = d[n][2];
+        s[1][2 * n + 1] = d[n][3];
+      }
     }
     float vf[4], vmax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
-      const float f = half_bits(cur.ks[i]) * (MODE ? 0.0625f * kScale : kScale);
+      const float f = half_bits(ks[i]) * (MODE ? 0.0625f * kScale : kScale);
       // a token that a row does not see counts as -inf whatever its scale holds
       s[0][i] = t < lim0 ? s[0][i] * f : -INFINITY;
       s[1][i] = t < lim1 ? s[1][i] * f : -INFINITY;
-      vf[i] = half_bits(cur.vs[i]) * (MODE ? 0.0625f : 1.0f);
+      vf[i] = half_bits(vs[i]) * (MODE ? 0.0625f : 1.0f);
       vmax = fmaxf(vmax, vf[i]);
     }
 #pragma unroll
@@ -175,8 +225,12 @@ __device__ __forceinline__ void attend(Smem &sh, int warp, int lane, const KvPla
     uint32_t ev[4][2], od[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      codes<MODE>(cur.vh[i].x, cur.vl[i].x, ev[i][0], od[i][0]);
-      codes<MODE>(cur.vh[i].y, cur.vl[i].y, ev[i][1], od[i][1]);
+      const int r = 2 * tig + (i & 1) + 8 * (i >> 1);  // 8 bytes at 8 gid of this token's row
+      const uint32_t at = cur + (MODE ? 2 : 1) * kPlane + (r >> 1) * kD + 8 * (gid & 1) +
+                          16 * ((((r & 1) << 2) | (gid >> 1)) ^ (((r >> 1) & 3) << 1));
+      const uint2 vh = lds64(at), vl = MODE ? lds64(at + kPlane) : make_uint2(0, 0);
+      codes<MODE>(vh.x, vl.x, ev[i][0], od[i][0]);
+      codes<MODE>(vh.y, vl.y, ev[i][1], od[i][1]);
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {  // plane byte 8 gid + mt: columns 16 gid + 2 mt, + 1
@@ -198,43 +252,45 @@ __device__ __forceinline__ void attend(Smem &sh, int warp, int lane, const KvPla
     }
   }
 
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// The state into slot `warp` of the shared memory.
+__device__ __forceinline__ void store_state(State &sh, Part &st, int warp, int lane) {
+  const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-    l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 1);
+    st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 2);
     if (tig == 0) {
-      sh.m[warp][gid + 8 * r] = m_run[r];
-      sh.l[warp][gid + 8 * r] = l_run[r];
+      sh.m[warp][gid + 8 * r] = st.m_run[r];
+      sh.l[warp][gid + 8 * r] = st.l_run[r];
     }
   }
-  const float up = pow2(e_run - 15);
+  const float up = pow2(st.e_run - 15);
 #pragma unroll
-  for (int mt = 0; mt < 8; ++mt) {
-    const int col = 16 * gid + 2 * mt;
+  for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      float *o0 = sh.o[warp][8 * nt + 2 * tig], *o1 = sh.o[warp][8 * nt + 2 * tig + 1];
-      o0[col] = o[mt][nt][0] * up;
-      o1[col] = o[mt][nt][1] * up;
-      o0[col + 1] = o[mt][nt][2] * up;
-      o1[col + 1] = o[mt][nt][3] * up;
-    }
-  }
+    for (int nt = 0; nt < 2; ++nt)
+      sh.o[warp][mt][nt][lane] = make_float4(st.o[mt][nt][0] * up, st.o[mt][nt][1] * up,
+                                             st.o[mt][nt][2] * up, st.o[mt][nt][3] * up);
 }
 
 // The parts: CTAs below p_ctas take (KV head, row group, part of the prefix),
 // the others (sequence, KV head, row tile, part of its own tokens).
 // part_lse [parts, B L H] (in units of log 2), part_o [parts, B L H, 128].
 template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Plan pl,
+__global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Plan pl,
                                                             float *__restrict__ part_lse,
                                                             float *__restrict__ part_o) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem &sh = *reinterpret_cast<Smem *>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2;
   const int64_t H = a.H, rows_out = a.B * a.L * H;
   const int Hkv = (int)a.Hkv, G = pl.G;
-  griddep_wait();
+  // Behind the tcgen05 kernel this one does not wait for it: that one began
+  // (and let this one begin) when all before it was complete.  Ending after it,
+  // as the join needs, is enough.
+  if (!pl.tc) griddep_wait();
   griddep_launch_dependents();
   int64_t cta = blockIdx.x;
   const bool prefix = cta < pl.p_ctas;
@@ -269,9 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Pl
     bi0 = b * a.L;
     row_base = b * a.cap * Hkv + j;
     const int len = (int)min((int64_t)a.len[b], a.cap);
-    if (len < 0) return;  // the sequence is not taking part
     t_begin = split * pl.o_len;
-    if (t_begin >= len) return;  // nor does the join read this part
+    if (t_begin >= len) {  // also a sequence that is not taking part: the join reads no such part
+      if (pl.tc) griddep_wait();
+      return;
+    }
     t_end = min(len, t_begin + pl.o_len);
     part = pl.p_splits + split;
     visible = len - (int)a.L + 1;
@@ -279,39 +337,63 @@ __global__ void __launch_bounds__(kThreads, 1) parts_kernel(PrefixAttnArgs a, Pl
   ways = kWarps / row_warps;
   const int rw = warp % row_warps, way = warp / row_warps;
   const int r0 = row0 + rw * kRows + gid, r1 = r0 + 8;
-  const uint16_t *q0 = r0 < R ? a.q + query_row(bi0, r0, G, H, j) * kD : nullptr;
-  const uint16_t *q1 = r1 < R ? a.q + query_row(bi0, r1, G, H, j) * kD : nullptr;
   const int lim0 = r0 >= R ? 0 : prefix ? visible : visible + r0 / G;
   const int lim1 = r1 >= R ? 0 : prefix ? visible : visible + r1 / G;
-  attend<MODE>(sh, warp, lane, prefix ? a.prefix : a.own, row_base, Hkv, t_begin, t_end, way, ways,
-               q0, q1, lim0, lim1);
-  __syncthreads();
-  for (int e = threadIdx.x; e < row_warps * kRows * (kD / 4); e += kThreads) {
-    const int r = e / (kD / 4), c4 = e % (kD / 4), w0 = r / kRows, rr = r % kRows;
-    if (row0 + r >= R) continue;
-    float M = -INFINITY;
-    for (int w = 0; w < ways; ++w) M = fmaxf(M, sh.m[w0 + w * row_warps][rr]);
-    float den = 0.0f;
-    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (M != -INFINITY)
-      for (int w = 0; w < ways; ++w) {
-        const int sw = w0 + w * row_warps;
-        if (sh.m[sw][rr] == -INFINITY) continue;
-        const float f = exp2_approx(sh.m[sw][rr] - M);
-        const float4 v = reinterpret_cast<const float4 *>(sh.o[sw][rr])[c4];
-        den += f * sh.l[sw][rr];
-        num.x += f * v.x;
-        num.y += f * v.y;
-        num.z += f * v.z;
-        num.w += f * v.w;
-      }
-    const int64_t at = (int64_t)part * rows_out + query_row(bi0, row0 + r, G, H, j);
-    if (c4 == 0) part_lse[at] = den > 0.0f ? M + log2f(den) : -INFINITY;
-    if (!(den > 0.0f)) continue;  // the join reads no output of a part without weight
-    const float inv = 1.0f / den;
-    reinterpret_cast<float4 *>(part_o + at * kD)[c4] =
-        make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+  uint4 *frag = reinterpret_cast<uint4 *>(smem_raw + rw * kFrag);
+  uint8_t *rest = smem_raw + row_warps * kFrag;
+  if (way == 0) {
+    uint32_t qa[8][4];
+    load_queries(qa, r0 < R ? a.q + query_row(bi0, r0, G, H, j) * kD : nullptr,
+                 r1 < R ? a.q + query_row(bi0, r1, G, H, j) * kD : nullptr, lane & 3);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) frag[k * 32 + lane] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
   }
+  __syncthreads();
+  Part st;
+  attend<MODE>(st, frag, smem_u32(rest + warp * kStages * stage_bytes(MODE)), lane,
+               prefix ? a.prefix : a.own, row_base, Hkv, t_begin, t_end, way, ways, lim0, lim1);
+  __syncthreads();  // the ring's place is free
+  State &sh = *reinterpret_cast<State *>(rest);
+  store_state(sh, st, warp, lane);
+  __syncthreads();
+  // the warps' states joined: a thread has two rows (8 nt + 2 (lane % 4), + 1) and
+  // four columns (16 (lane / 4) + 4 mp ..) of a row tile at a time
+  for (int e = threadIdx.x; e < row_warps * 8 * 32; e += kThreads) {
+    const int l = e & 31, nt = (e >> 5) & 1, mp = (e >> 6) & 3, w0 = e >> 8;
+    const int rr = 8 * nt + 2 * (l & 3);
+    if (row0 + w0 * kRows + rr >= R) continue;
+    float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.0f, 0.0f}, num[2][4] = {};
+    for (int w = 0; w < ways; ++w)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) M[i] = fmaxf(M[i], sh.m[w0 + w * row_warps][rr + i]);
+    for (int w = 0; w < ways; ++w) {
+      const int sw = w0 + w * row_warps;
+      const float4 a4 = sh.o[sw][2 * mp][nt][l], b4 = sh.o[sw][2 * mp + 1][nt][l];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (sh.l[sw][rr + i] == 0.0f) continue;  // saw no token (NaN scores make l NaN)
+        const float f = exp2_approx(sh.m[sw][rr + i] - M[i]);
+        den[i] += f * sh.l[sw][rr + i];
+        num[i][0] += f * (i ? a4.y : a4.x);
+        num[i][1] += f * (i ? a4.w : a4.z);
+        num[i][2] += f * (i ? b4.y : b4.x);
+        num[i][3] += f * (i ? b4.w : b4.z);
+      }
+    }
+    const int col = 16 * (l >> 2) + 4 * mp;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = row0 + w0 * kRows + rr + i;
+      if (r >= R) continue;
+      const int64_t at = (int64_t)part * rows_out + query_row(bi0, r, G, H, j);
+      if (col == 0) part_lse[at] = den[i] == 0.0f ? -INFINITY : M[i] + log2f(den[i]);
+      if (den[i] == 0.0f) continue;  // the join reads no output of a part without weight
+      const float inv = 1.0f / den[i];
+      *reinterpret_cast<float4 *>(part_o + at * kD + col) =
+          make_float4(num[i][0] * inv, num[i][1] * inv, num[i][2] * inv, num[i][3] * inv);
+    }
+  }
+  if (pl.tc) griddep_wait();
 }
 
 // One warp per output row: lane s holds the weights of parts s, s + 32, ..
@@ -336,20 +418,25 @@ __global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, Plan pl,
   const int parts = np + own;
   auto slot = [&](int s) { return (int64_t)(s < np ? s : pl.p_splits + s - np) * rows + row; };
   float M = -INFINITY;
-  for (int s = lane; s < parts; s += 32) M = fmaxf(M, part_lse[slot(s)]);
+  bool nan = false;  // fmaxf passes over NaN, which the output must show
+  for (int s = lane; s < parts; s += 32) {
+    const float v = part_lse[slot(s)];
+    M = fmaxf(M, v);
+    nan |= v != v;
+  }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  if (__any_sync(0xffffffffu, nan)) M = 0.0f;
   float den = 0.0f, o[4] = {};
   if (M != -INFINITY)
     for (int s0 = 0; s0 < parts; s0 += 32) {
       const int n = min(32, parts - s0);
       const float f = lane < n ? exp2f(part_lse[slot(s0 + lane)] - M) : 0.0f;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < n; ++s) {
         const float w = __shfl_sync(0xffffffffu, f, s);
-        // the output of a part without weight is not written
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (w != 0.0f) v = reinterpret_cast<const float4 *>(part_o + slot(s0 + s) * kD)[lane];
+        float4 v = reinterpret_cast<const float4 *>(part_o + slot(s0 + s) * kD)[lane];
+        if (w == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // a part without weight writes none
         den += w;
         o[0] += w * v.x;
         o[1] += w * v.y;
@@ -378,7 +465,10 @@ Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t 
     p.tc_groups = (int)((R + kTcRows - 1) / kTcRows);
     p.tc_tiles = (int)((P + kTcTokens - 1) / kTcTokens);
     p.tc_units = Hkv * p.tc_groups * p.tc_tiles;
-    p.tc_ctas = (int)min((int64_t)kSms, p.tc_units);
+    // as many CTAs as the longest run of units needs: fewer parts to join, and
+    // SMs for the own tokens
+    const int64_t run = (p.tc_units + kSms - 1) / kSms;
+    p.tc_ctas = (int)((p.tc_units + run - 1) / run);
     for (int64_t item = 0; item < Hkv * p.tc_groups; ++item)
       p.p_splits = max(p.p_splits, tc_parts(p, item));
     p.p_groups = 0;
@@ -438,7 +528,7 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
   }
   if (ctas > 0) {
     auto kern = a.mode ? pattn::parts_kernel<1> : pattn::parts_kernel<0>;
-    constexpr int smem = (int)sizeof(pattn::Smem);
+    const int smem = pattn::smem_bytes(a.mode, p.p_ctas > 0 ? p.row_warps : 1);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)ctas), dim3(pattn::kThreads), smem, st, true, a, p, lse, o);

@@ -48,6 +48,31 @@ __device__ __forceinline__ uint32_t pair(uint32_t x, uint32_t y, int b) {
   return r;
 }
 
+// Eight columns (one word of each plane) as fp16 codes in the order 0 2 4 6 1 3 5 7.
+template <int MODE>
+__device__ __forceinline__ uint4 codes8(uint32_t hw, uint32_t lw) {
+  uint32_t ev, od;
+  codes<MODE>(hw, lw, ev, od);
+  constexpr uint32_t kOff = MODE ? 0xE488E488u : 0xE408E408u;  // -(1024 + offset)
+  uint4 r;
+  const uint32_t t[4] = {prmt(ev, 0x64646464u, 0x4140), prmt(ev, 0x64646464u, 0x4342),
+                         prmt(od, 0x64646464u, 0x4140), prmt(od, 0x64646464u, 0x4342)};
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"(t[0]), "r"(kOff));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.y) : "r"(t[1]), "r"(kOff));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.z) : "r"(t[2]), "r"(kOff));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.w) : "r"(t[3]), "r"(kOff));
+  return r;
+}
+
+// pair(x, y, b) and pair(x, y, b + 1)
+template <int MODE>
+__device__ __forceinline__ void pair2(uint32_t (&r)[2], uint32_t x, uint32_t y, int b) {
+  const uint32_t z = prmt(x, y, b ? 0x7362u : 0x5140u);  // x_b, y_b, x_b+1, y_b+1
+  constexpr uint32_t kOff = MODE ? 0xE488E488u : 0xE408E408u;  // -(1024 + offset)
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[0]) : "r"(prmt(z, 0x64646464u, 0x4140)), "r"(kOff));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[1]) : "r"(prmt(z, 0x64646464u, 0x4342)), "r"(kOff));
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);

@@ -25,6 +25,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;   // tokens a warp takes at a time
 constexpr int kRows = 16;   // rows of a warp
 constexpr int kMinExp = -40;  // below any fp16 scale / 16
+constexpr float kSlack = 8.0f;
+constexpr int kHead = 7;  // p v_scale < 2^(8 + 7)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
 
@@ -59,56 +61,82 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool i
                : "memory");
 }
 
-// One tile's copies for one lane: of each plane the 16-byte pieces of rows
-// lane / 4 and 8 + lane / 4.  A row's pieces lie together; V's are exchanged so
-// that the lanes that read a column's 8 bytes of four row pairs find them in
-// different banks.  The scale of K (lanes 0 to 15) or V (16 to 31) of token
-// lane % 16 is returned.  Tokens at or past t_end are zeros.
+// A warp's way through a cache's rows, for one lane: of each plane's tile it
+// copies the 16-byte pieces lane % 4 of rows lane / 4 and 8 + lane / 4, and it
+// reads the scale of K (lanes 0 to 15) or V (16 to 31) of token lane % 16.  A
+// row's pieces lie together; V's are exchanged so that the lanes that read a
+// column's 8 bytes of four row pairs find them in different banks.  Tokens at
+// or past the end are zeros.
 template <int MODE>
-__device__ __forceinline__ uint16_t load_tile(uint32_t stage, int t0, int t_end, int64_t row_base,
-                                              int Hkv, int lane, const KvPlanes &c) {
-  constexpr int kPlane = kTile * (kD / 2);
+struct Loader {
+  static constexpr int kPlane = kTile * (kD / 2);
+  const KvPlanes &c;
+  const uint16_t *scale;
+  int64_t off, next, half, scale_off, scale_next;  // bytes, and scales
+  int t, end, stride;                              // row lane / 4's token
+  uint32_t kd, vd[2];
+  __device__ __forceinline__ Loader(const KvPlanes &c, int t0, int t_end, int step_tokens,
+                                    int64_t row_base, int Hkv, int lane)
+      : c(c), end(t_end), stride(step_tokens) {
+    const int r = lane >> 2, p = lane & 3;
+    t = t0 + r;
+    off = (row_base + (int64_t)t * Hkv) * (kD / 2) + 16 * p;
+    next = (int64_t)step_tokens * Hkv * (kD / 2);
+    half = (int64_t)8 * Hkv * (kD / 2);
+    scale = lane < 16 ? c.k_scale : c.v_scale;
+    scale_off = row_base + (int64_t)(t0 + (lane & 15)) * Hkv;
+    scale_next = (int64_t)step_tokens * Hkv;
+    kd = r * (kD / 2) + 16 * p;
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const int r = 8 * n + (lane >> 2), p = lane & 3, t = t0 + r;
-    const bool in = t < t_end;
-    const int64_t off = in ? (row_base + (int64_t)t * Hkv) * (kD / 2) + 16 * p : 0;
-    const uint32_t kd = stage + r * (kD / 2) + 16 * p;
-    const uint32_t vd = stage + (MODE ? 2 : 1) * kPlane + (r >> 1) * kD +
-                        16 * ((((r & 1) << 2) | p) ^ (((r >> 1) & 3) << 1));
-    cp_async16(kd, c.k_hi + off, in);
-    if (MODE) cp_async16(kd + kPlane, c.k_lo + off, in);
-    cp_async16(vd, c.v_hi + off, in);
-    if (MODE) cp_async16(vd + kPlane, c.v_lo + off, in);
+    for (int n = 0; n < 2; ++n) {
+      const int q = r + 8 * n;
+      vd[n] = (MODE ? 2 : 1) * kPlane + (q >> 1) * kD +
+              16 * ((((q & 1) << 2) | p) ^ (((q >> 1) & 3) << 1));
+    }
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  const int t = t0 + (lane & 15);
-  return t < t_end ? __ldg((lane < 16 ? c.k_scale : c.v_scale) + row_base + (int64_t)t * Hkv)
-                   : (uint16_t)0;
-}
+  // The next tile into the stage at `at`; its scale.
+  __device__ __forceinline__ uint16_t operator()(uint32_t at, int lane) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const bool in = t + 8 * n < end;
+      const int64_t o = in ? off + n * half : 0;
+      cp_async16(at + kd + n * 8 * (kD / 2), c.k_hi + o, in);
+      if (MODE) cp_async16(at + kd + n * 8 * (kD / 2) + kPlane, c.k_lo + o, in);
+      cp_async16(at + vd[n], c.v_hi + o, in);
+      if (MODE) cp_async16(at + vd[n] + kPlane, c.v_lo + o, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    uint16_t s = 0;
+    if (t - (lane >> 2) + (lane & 15) < end) s = __ldg(scale + scale_off);
+    t += stride;
+    off += next;
+    scale_off += scale_next;
+    return s;
+  }
+};
 
-// One part for a tile of 16 rows (queries at `frag`): tokens t_begin +
-// 16 (first + n step) .. of the rows' cache, row r seeing tokens below lim(r).
-// The state is left in the registers' layout for store_state.
+// One part for a tile of 16 rows (queries at `frag`): every tile of `load`, row
+// r seeing tokens below lim(r).  As on the tcgen05 path p is kept as 2^(s -
+// shift), shift = m + e - kHead with m a maximum at most kSlack behind and 2^e
+// above every V scale so far: the output is rescaled only when one of them has
+// grown, and p v_scale < 2^15 enters the product as one fp16 term (11 bits:
+// 2^-12 of each weight at most, as the fp16 output's own rounding is).
 struct Part {
-  float m_run[2], l_run[2];
-  float o[8][2][4];  // O^T: columns tile mt, rows tile nt
-  int e_run;         // o holds the output in units of 2^(e_run - 15)
+  float shift[2], l_run[2];  // rows lane / 4, + 8
+  float o[8][2][4];          // O^T: columns tile mt, rows tile nt
 };
 template <int MODE>
-__device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t ring, int lane,
-                                       const KvPlanes &c, int64_t row_base, int Hkv, int t_begin,
-                                       int t_end, int first, int step, int lim0, int lim1) {
+__device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE> &load,
+                                       uint32_t ring, uint16_t (&sc)[kStages], int lane, int t0,
+                                       int t_end, int stride, int lim0, int lim1) {
   constexpr int kPlane = kTile * (kD / 2);
   const int gid = lane >> 2, tig = lane & 3;
   lim0 = min(lim0, t_end);
   lim1 = min(lim1, t_end);
-  float(&m_run)[2] = st.m_run, (&l_run)[2] = st.l_run;  // rows gid, gid + 8
-  float(&o)[8][2][4] = st.o;
-  int &e_run = st.e_run;
-  m_run[0] = m_run[1] = -INFINITY;
-  l_run[0] = l_run[1] = 0.0f;
-  e_run = kMinExp;
+  float(&shift)[2] = st.shift, (&l_run)[2] = st.l_run, (&o)[8][2][4] = st.o;
+  float m[2] = {-INFINITY, -INFINITY};
+  int e_run = kMinExp;
+  shift[0] = shift[1] = l_run[0] = l_run[1] = 0.0f;
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -116,18 +144,11 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t rin
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
-  const int stride = step * kTile;
-  int t0 = t_begin + first * kTile;
-  uint16_t sc[kStages];  // of the tiles in the ring, the oldest first
-#pragma unroll
-  for (int i = 0; i + 1 < kStages; ++i)
-    sc[i] = load_tile<MODE>(ring + i * stage_bytes(MODE), t0 + i * stride, t_end, row_base, Hkv, lane, c);
   for (int slot = 0; t0 < t_end; t0 += stride) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();  // this tile is here, and every lane is done with the one before
     const int free = slot == 0 ? kStages - 1 : slot - 1;
-    sc[kStages - 1] = load_tile<MODE>(ring + free * stage_bytes(MODE), t0 + (kStages - 1) * stride,
-                                      t_end, row_base, Hkv, lane, c);
+    sc[kStages - 1] = load(ring + free * stage_bytes(MODE), lane);
     const uint32_t cur = ring + slot * stage_bytes(MODE);
     slot = slot == kStages - 1 ? 0 : slot + 1;
     uint16_t ks[4], vs[4];
@@ -155,10 +176,9 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t rin
         for (int n = 0; n < 2; ++n) {
           const uint32_t hw[4] = {kh[n].x, kh[n].y, kh[n].z, kh[n].w};
           const uint32_t lw[4] = {kl[n].x, kl[n].y, kl[n].z, kl[n].w};
-          uint32_t ev, od;
-          codes<MODE>(hw[w], lw[w], ev, od);
-          mma_f16(d[n], q0.x, q0.y, q0.z, q0.w, pair<MODE>(ev, od, 0), pair<MODE>(ev, od, 1));
-          mma_f16(d[n], q1.x, q1.y, q1.z, q1.w, pair<MODE>(ev, od, 2), pair<MODE>(ev, od, 3));
+          const uint4 u = codes8<MODE>(hw[w], lw[w]);
+          mma_f16(d[n], q0.x, q0.y, q0.z, q0.w, u.x, u.y);
+          mma_f16(d[n], q1.x, q1.y, q1.z, q1.w, u.z, u.w);
         }
       }
 #pragma unroll
@@ -169,7 +189,7 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t rin
         s[1][2 * n + 1] = d[n][3];
       }
     }
-    float vf[4], vmax = 0.0f;
+    float vf[4], vmax = 0.0f, tmax[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
@@ -179,49 +199,58 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t rin
       s[1][i] = t < lim1 ? s[1][i] * f : -INFINITY;
       vf[i] = half_bits(vs[i]) * (MODE ? 0.0625f : 1.0f);
       vmax = fmaxf(vmax, vf[i]);
+      tmax[0] = fmaxf(tmax[0], s[0][i]);
+      tmax[1] = fmaxf(tmax[1], s[1][i]);
     }
 #pragma unroll
-    for (int x = 1; x <= 2; x <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, x));
-    // 2^e: the largest v scale so far in [1/2, 1), times 2^15: p v_scale enters
-    // the product as one fp16 term (11 bits: 2^-12 of each weight at most, as
-    // the fp16 output's own rounding is), 2^29 above the fp16 subnormals
+    for (int x = 1; x <= 2; x <<= 1) {
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, x));
+      tmax[0] = fmaxf(tmax[0], __shfl_xor_sync(0xffffffffu, tmax[0], x));
+      tmax[1] = fmaxf(tmax[1], __shfl_xor_sync(0xffffffffu, tmax[1], x));
+    }
     const int e_tile = vmax > 0.0f ? (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126 : kMinExp;
     const int e_new = min(100, max(e_run, e_tile));
-    const float unit = pow2(max(e_run - e_new, -126));
-    const float down = pow2(15 - e_new);
-    e_run = e_new;
-    float corr[2];
+    if (__any_sync(0xffffffffu, tmax[0] > m[0] + kSlack || tmax[1] > m[1] + kSlack || e_new > e_run)) {
+      float corr[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float old = shift[r];
+        const bool fresh = m[r] == -INFINITY;  // a row that has seen no token: nothing to rescale
+        if (tmax[r] > m[r] + kSlack) m[r] = tmax[r];
+        shift[r] = m[r] == -INFINITY ? 0.0f : m[r] + (float)(e_new - kHead);
+        corr[r] = fresh ? 1.0f : exp2_approx(old - shift[r]);
+        l_run[r] *= corr[r];
+      }
+      e_run = e_new;
+      // rows 8 nt + 2 tig, + 1 of O^T's columns: their corr is in lanes 8 tig, 8 tig + 4
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float c0 = __shfl_sync(0xffffffffu, corr[nt], 8 * tig);
+        const float c1 = __shfl_sync(0xffffffffu, corr[nt], 8 * tig + 4);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          o[mt][nt][0] *= c0;
+          o[mt][nt][1] *= c1;
+          o[mt][nt][2] *= c0;
+          o[mt][nt][3] *= c1;
+        }
+      }
+    }
     uint32_t pb[2][2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float tmax = fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3]));
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-      const float m_new = fmaxf(m_run[r], tmax);
-      const bool live = m_new != -INFINITY;  // a row that has seen a token
-      corr[r] = live ? exp2_approx(m_run[r] - m_new) : 1.0f;
       float p[4], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = s[r][i] != -INFINITY ? exp2_approx(s[r][i] - m_new) : 0.0f;
+        const bool seen = s[r][i] != -INFINITY;
+        p[i] = seen ? exp2_approx(s[r][i] - shift[r]) : 0.0f;
         sum += p[i];
-        p[i] = s[r][i] != -INFINITY ? p[i] * (vf[i] * down) : 0.0f;
+        p[i] = seen ? p[i] * vf[i] : 0.0f;
       }
-      l_run[r] = l_run[r] * corr[r] + sum;  // this lane's tokens only
-      m_run[r] = m_new;
+      l_run[r] += sum;  // this lane's tokens only
       pb[r][0] = pack_half2(p[0], p[1]);
       pb[r][1] = pack_half2(p[2], p[3]);
     }
-    // rows 8 nt + 2 tig, + 1 of O^T's columns: their corr is in lanes 8 tig, 8 tig + 4
-    float cr[2][2];
-    bool rescale = false;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      cr[nt][0] = __shfl_sync(0xffffffffu, corr[nt], 8 * tig) * unit;
-      cr[nt][1] = __shfl_sync(0xffffffffu, corr[nt], 8 * tig + 4) * unit;
-      rescale |= cr[nt][0] != 1.0f || cr[nt][1] != 1.0f;
-    }
-    rescale = __any_sync(0xffffffffu, rescale);
     uint32_t ev[4][2], od[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -233,25 +262,20 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, uint32_t rin
       codes<MODE>(vh.y, vl.y, ev[i][1], od[i][1]);
     }
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {  // plane byte 8 gid + mt: columns 16 gid + 2 mt, + 1
-      const int w = mt >> 2, b = mt & 3;
-      const uint32_t a0 = pair<MODE>(ev[0][w], ev[1][w], b);
-      const uint32_t a1 = pair<MODE>(od[0][w], od[1][w], b);
-      const uint32_t a2 = pair<MODE>(ev[2][w], ev[3][w], b);
-      const uint32_t a3 = pair<MODE>(od[2][w], od[3][w], b);
+    for (int h = 0; h < 4; ++h) {  // plane bytes 8 gid + 2 h, + 1: columns 16 gid + 4 h .. + 3
+      const int w = h >> 1, b = 2 * (h & 1);
+      uint32_t a[4][2];
+      pair2<MODE>(a[0], ev[0][w], ev[1][w], b);
+      pair2<MODE>(a[1], od[0][w], od[1][w], b);
+      pair2<MODE>(a[2], ev[2][w], ev[3][w], b);
+      pair2<MODE>(a[3], od[2][w], od[3][w], b);
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        if (rescale) {
-          o[mt][nt][0] *= cr[nt][0];
-          o[mt][nt][1] *= cr[nt][1];
-          o[mt][nt][2] *= cr[nt][0];
-          o[mt][nt][3] *= cr[nt][1];
-        }
-        mma_f16(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+          mma_f16(o[2 * h + i][nt], a[0][i], a[1][i], a[2][i], a[3][i], pb[nt][0], pb[nt][1]);
     }
   }
-
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
@@ -263,17 +287,15 @@ __device__ __forceinline__ void store_state(State &sh, Part &st, int warp, int l
     st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 1);
     st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 2);
     if (tig == 0) {
-      sh.m[warp][gid + 8 * r] = st.m_run[r];
+      sh.m[warp][gid + 8 * r] = st.shift[r];
       sh.l[warp][gid + 8 * r] = st.l_run[r];
     }
   }
-  const float up = pow2(st.e_run - 15);
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
-      sh.o[warp][mt][nt][lane] = make_float4(st.o[mt][nt][0] * up, st.o[mt][nt][1] * up,
-                                             st.o[mt][nt][2] * up, st.o[mt][nt][3] * up);
+      sh.o[warp][mt][nt][lane] = make_float4(st.o[mt][nt][0], st.o[mt][nt][1], st.o[mt][nt][2], st.o[mt][nt][3]);
 }
 
 // The parts: CTAs below p_ctas take (KV head, row group, part of the prefix),
@@ -341,57 +363,83 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
   const int lim1 = r1 >= R ? 0 : prefix ? visible : visible + r1 / G;
   uint4 *frag = reinterpret_cast<uint4 *>(smem_raw + rw * kFrag);
   uint8_t *rest = smem_raw + row_warps * kFrag;
+  const uint32_t ring = smem_u32(rest + warp * kStages * stage_bytes(MODE));
+  const int t0 = t_begin + way * kTile, stride = ways * kTile;
+  Loader<MODE> load(prefix ? a.prefix : a.own, t0, t_end, stride, row_base, Hkv, lane);
+  uint16_t sc[kStages];  // scales of the tiles in the ring, the oldest first
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) sc[i] = load(ring + i * stage_bytes(MODE), lane);
   if (way == 0) {
     uint32_t qa[8][4];
     load_queries(qa, r0 < R ? a.q + query_row(bi0, r0, G, H, j) * kD : nullptr,
                  r1 < R ? a.q + query_row(bi0, r1, G, H, j) * kD : nullptr, lane & 3);
+    // columns 0 2 4 6 1 3 5 7 of each 8, as codes8 gives them: the even ones are
+    // k-step 2 w's, the odd ones 2 w + 1's
 #pragma unroll
-    for (int k = 0; k < 8; ++k) frag[k * 32 + lane] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        const uint32_t sel = odd ? 0x7632u : 0x5410u;
+        frag[(2 * w + odd) * 32 + lane] =
+            make_uint4(prmt(qa[2 * w][0], qa[2 * w][2], sel), prmt(qa[2 * w][1], qa[2 * w][3], sel),
+                       prmt(qa[2 * w + 1][0], qa[2 * w + 1][2], sel),
+                       prmt(qa[2 * w + 1][1], qa[2 * w + 1][3], sel));
+      }
   }
   __syncthreads();
   Part st;
-  attend<MODE>(st, frag, smem_u32(rest + warp * kStages * stage_bytes(MODE)), lane,
-               prefix ? a.prefix : a.own, row_base, Hkv, t_begin, t_end, way, ways, lim0, lim1);
+  attend<MODE>(st, frag, load, ring, sc, lane, t0, t_end, stride, lim0, lim1);
   __syncthreads();  // the ring's place is free
   State &sh = *reinterpret_cast<State *>(rest);
   store_state(sh, st, warp, lane);
   __syncthreads();
-  // the warps' states joined: a thread has two rows (8 nt + 2 (lane % 4), + 1) and
-  // four columns (16 (lane / 4) + 4 mp ..) of a row tile at a time
+  // the warps' states joined by rows' factors 2^(shift_w - M) / den (0 for a
+  // warp that saw no token; NaN scores make l NaN)
+  if (threadIdx.x < row_warps * kRows) {
+    const int w0 = threadIdx.x / kRows, rr = threadIdx.x % kRows, r = row0 + threadIdx.x;
+    float M = -INFINITY, den = 0.0f;
+    for (int w = w0; w < kWarps; w += row_warps)
+      if (sh.l[w][rr] != 0.0f) M = fmaxf(M, sh.m[w][rr]);
+    for (int w = w0; w < kWarps; w += row_warps) {
+      const float l = sh.l[w][rr];
+      const float f = l == 0.0f ? 0.0f : exp2_approx(sh.m[w][rr] - M);
+      den += f * l;
+      sh.m[w][rr] = f;
+    }
+    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+    for (int w = w0; w < kWarps; w += row_warps) sh.m[w][rr] *= inv;
+    if (r < R)
+      part_lse[(int64_t)part * rows_out + query_row(bi0, r, G, H, j)] =
+          den == 0.0f ? -INFINITY : M + log2f(den);
+  }
+  __syncthreads();
+  // a thread has two rows (8 nt + 2 (lane % 4), + 1) and four columns (16 (lane / 4)
+  // + 4 mp ..) of a row tile at a time
   for (int e = threadIdx.x; e < row_warps * 8 * 32; e += kThreads) {
     const int l = e & 31, nt = (e >> 5) & 1, mp = (e >> 6) & 3, w0 = e >> 8;
-    const int rr = 8 * nt + 2 * (l & 3);
-    if (row0 + w0 * kRows + rr >= R) continue;
-    float M[2] = {-INFINITY, -INFINITY}, den[2] = {0.0f, 0.0f}, num[2][4] = {};
-    for (int w = 0; w < ways; ++w)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) M[i] = fmaxf(M[i], sh.m[w0 + w * row_warps][rr + i]);
-    for (int w = 0; w < ways; ++w) {
-      const int sw = w0 + w * row_warps;
-      const float4 a4 = sh.o[sw][2 * mp][nt][l], b4 = sh.o[sw][2 * mp + 1][nt][l];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (sh.l[sw][rr + i] == 0.0f) continue;  // saw no token (NaN scores make l NaN)
-        const float f = exp2_approx(sh.m[sw][rr + i] - M[i]);
-        den[i] += f * sh.l[sw][rr + i];
-        num[i][0] += f * (i ? a4.y : a4.x);
-        num[i][1] += f * (i ? a4.w : a4.z);
-        num[i][2] += f * (i ? b4.y : b4.x);
-        num[i][3] += f * (i ? b4.w : b4.z);
-      }
+    const int rr = 8 * nt + 2 * (l & 3), r0 = row0 + w0 * kRows + rr;
+    if (r0 >= R) continue;
+    float num[2][4] = {};
+#pragma unroll 4
+    for (int w = w0; w < kWarps; w += row_warps) {
+      const float4 a4 = sh.o[w][2 * mp][nt][l], b4 = sh.o[w][2 * mp + 1][nt][l];
+      const float2 f = *reinterpret_cast<const float2 *>(&sh.m[w][rr]);
+      num[0][0] += f.x * a4.x;
+      num[0][1] += f.x * a4.z;
+      num[0][2] += f.x * b4.x;
+      num[0][3] += f.x * b4.z;
+      num[1][0] += f.y * a4.y;
+      num[1][1] += f.y * a4.w;
+      num[1][2] += f.y * b4.y;
+      num[1][3] += f.y * b4.w;
     }
-    const int col = 16 * (l >> 2) + 4 * mp;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + w0 * kRows + rr + i;
-      if (r >= R) continue;
-      const int64_t at = (int64_t)part * rows_out + query_row(bi0, r, G, H, j);
-      if (col == 0) part_lse[at] = den[i] == 0.0f ? -INFINITY : M[i] + log2f(den[i]);
-      if (den[i] == 0.0f) continue;  // the join reads no output of a part without weight
-      const float inv = 1.0f / den[i];
-      *reinterpret_cast<float4 *>(part_o + at * kD + col) =
-          make_float4(num[i][0] * inv, num[i][1] * inv, num[i][2] * inv, num[i][3] * inv);
-    }
+    for (int i = 0; i < 2; ++i)
+      if (r0 + i < R)
+        *reinterpret_cast<float4 *>(part_o +
+                                    ((int64_t)part * rows_out + query_row(bi0, r0 + i, G, H, j)) * kD +
+                                    16 * (l >> 2) + 4 * mp) =
+            make_float4(num[i][0], num[i][1], num[i][2], num[i][3]);
   }
   if (pl.tc) griddep_wait();
 }
@@ -473,7 +521,7 @@ Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t 
       p.p_splits = max(p.p_splits, tc_parts(p, item));
     p.p_groups = 0;
   } else if (P > 0) {
-    int64_t s = (2 * 148 + Hkv * p.p_groups - 1) / (Hkv * p.p_groups);
+    int64_t s = (2 * kSms + Hkv * p.p_groups - 1) / (Hkv * p.p_groups);
     s = min(s, (P + 4 * step - 1) / (4 * step));
     s = max((int64_t)1, min(s, (int64_t)64));
     p.p_len = (int)(((P + s - 1) / s + step - 1) / step * step);
@@ -483,7 +531,7 @@ Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t 
   p.o_tiles = (int)((L * p.G + kRows - 1) / kRows);
   if (cap > 0) {
     const int64_t base = B * Hkv * p.o_tiles;
-    int64_t s = max((int64_t)1, (4 * 148 + base - 1) / base);
+    int64_t s = max((int64_t)1, (2 * kSms + base - 1) / base);
     s = min(s, (cap + 255) / 256);
     p.o_len = (int)(((cap + s - 1) / s + 127) / 128 * 128);
     p.o_splits = (int)((cap + p.o_len - 1) / p.o_len);

@@ -85,22 +85,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Eight columns (one word of each plane) as fp16 codes in the order 0 2 4 6 1 3 5 7.
-template <int MODE>
-__device__ __forceinline__ uint4 codes8(uint32_t hw, uint32_t lw) {
-  uint32_t ev, od;
-  codes<MODE>(hw, lw, ev, od);
-  constexpr uint32_t kOff = MODE ? 0xE488E488u : 0xE408E408u;  // -(1024 + offset)
-  uint4 r;
-  const uint32_t t[4] = {prmt(ev, 0x64646464u, 0x4140), prmt(ev, 0x64646464u, 0x4342),
-                         prmt(od, 0x64646464u, 0x4140), prmt(od, 0x64646464u, 0x4342)};
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"(t[0]), "r"(kOff));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.y) : "r"(t[1]), "r"(kOff));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.z) : "r"(t[2]), "r"(kOff));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r.w) : "r"(t[3]), "r"(kOff));
-  return r;
-}
-
 // One thread's share of a tile's plane rows: for q = 0 .. 3, 16 bytes (piece
 // tid / 8 % 4) of the row of token 32 q + 8 (tid / 32) + tid % 8.
 struct Words {

@@ -22,7 +22,7 @@ constexpr int kWarps = 8;
 constexpr int kTokens = 32;  // of a warp
 
 template <int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a, int G, int ways) {
+__global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a, int lgG, int ways) {
   __shared__ float part[kWarps][kTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
@@ -32,8 +32,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
   const int j = (int)(blockIdx.y % a.Hkv);
   const int64_t b = blockIdx.y / a.Hkv;  // 0 where the cache is shared
   const int len = own ? (int)min((int64_t)a.len[b], a.cap) : (int)a.cap;
-  const int R = (int)((own ? a.L : a.B * a.L) * G);
-  const int64_t bi0 = b * a.L;
+  const int R = (int)(own ? a.L : a.B * a.L) << lgG;
+  const int bi0 = (int)(b * a.L);
   const int tw = warp / ways, way = warp % ways;  // token group of the CTA, share of the rows
   const int t0 = (blockIdx.x * (kWarps / ways) + tw) * kTokens;
   const bool some = t0 < len;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
     }
     for (int r = way * 16; r < R; r += ways * 16) {
       const int r0 = r + gid, r1 = r0 + 8;
-      const int64_t at0 = query_row(bi0, r0, G, a.H, j), at1 = query_row(bi0, r1, G, a.H, j);
+      const int64_t at0 = query_row(bi0, r0, lgG, (int)a.H, j), at1 = query_row(bi0, r1, lgG, (int)a.H, j);
       uint32_t qa[8][4];
       load_queries(qa, r0 < R ? a.q + at0 * kD : nullptr, r1 < R ? a.q + at1 * kD : nullptr, tig);
       // a row without weight (lse -inf) gives none
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
       const float b0 = e0 == -INFINITY ? INFINITY : e0 * kLog2e;
       const float b1 = e1 == -INFINITY ? INFINITY : e1 * kLog2e;
       // own tokens: query i sees those below len - L + 1 + i
-      const int lim0 = own ? len - (int)a.L + 1 + r0 / G : len;
-      const int lim1 = own ? len - (int)a.L + 1 + r1 / G : len;
+      const int lim0 = own ? len - (int)a.L + 1 + (r0 >> lgG) : len;
+      const int lim1 = own ? len - (int)a.L + 1 + (r1 >> lgG) : len;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -417,7 +417,10 @@ __global__ void __launch_bounds__(256) gather_kernel(KvEvictArgs a, int runs) {
 cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st) {
   const int G = (int)(a.H / a.Hkv);
   const int64_t R = (a.len ? a.L : a.B * a.L) * G;
-  if (!a.len && R >= 128) return evict::launch_weights_tc(a, st);
+  if (!a.len && R >= 128 && a.Hkv * ((a.cap + 127) / 128) <= 0x3fffffff)
+    return evict::launch_weights_tc(a, st);
+  int lgG = 0;
+  while ((1 << lgG) < G) ++lgG;
   // The warps of a CTA share the rows of its tokens when there are more rows
   // than a warp's pass and too few tokens to give every warp its own.
   const int64_t caches = (a.len ? a.B : 1) * a.Hkv;
@@ -428,7 +431,7 @@ cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st) {
   const int64_t span = (evict::kWarps / ways) * evict::kTokens;
   const dim3 grid((unsigned)((a.cap + span - 1) / span), (unsigned)caches);
   auto kern = a.mode ? evict::weights_kernel<1> : evict::weights_kernel<0>;
-  return launch_pdl(kern, grid, dim3(evict::kWarps * 32), 0, st, true, a, G, ways);
+  return launch_pdl(kern, grid, dim3(evict::kWarps * 32), 0, st, true, a, lgG, ways);
 }
 
 cudaError_t launch_kv_evict(const KvEvictArgs &a, cudaStream_t st) {

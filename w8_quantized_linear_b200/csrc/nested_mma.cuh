@@ -89,10 +89,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// Query rows of one KV head: row r is query r / G of the tile's first query
-// bi0 (a query is one token of one sequence) and head j * G + r % G.
-__device__ __forceinline__ int64_t query_row(int64_t bi0, int r, int G, int64_t H, int j) {
-  return (bi0 + r / G) * H + (int64_t)j * G + r % G;
+// Query rows of one KV head j: row r is query r >> lgG of the tile's first
+// query bi0 (a query is one token of one sequence) and head (j << lgG) + its low
+// lgG bits.
+__device__ __forceinline__ int64_t query_row(int bi0, int r, int lgG, int H, int j) {
+  return (int64_t)(bi0 + (r >> lgG)) * H + (j << lgG) + (r & ((1 << lgG) - 1));
 }
 
 // The A operand of the scores for row gid (p0) and gid + 8 (p1) of a 16-row

@@ -121,26 +121,34 @@ struct Loader {
 // above every V scale so far: the output is rescaled only when one of them has
 // grown, and p v_scale < 2^15 enters the product as one fp16 term (11 bits:
 // 2^-12 of each weight at most, as the fp16 output's own rounding is).
+// e with vmax < 2^e, at most 100 (an infinite scale)
+__device__ __forceinline__ int e_tile_of(float vmax) {
+  return vmax > 0.0f ? min(100, (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126) : kMinExp;
+}
+template <int NT>  // row tiles of 8: 1 where there are no more than 8 rows
 struct Part {
-  float shift[2], l_run[2];  // rows lane / 4, + 8
-  float o[8][2][4];          // O^T: columns tile mt, rows tile nt
+  float shift[NT], l_run[NT];  // rows lane / 4, + 8
+  float o[8][NT][4];           // O^T: columns tile mt, rows tile nt
 };
-template <int MODE>
-__device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE> &load,
+template <int MODE, int NT>
+__device__ __forceinline__ void attend(Part<NT> &st, const uint4 *frag, Loader<MODE> &load,
                                        uint32_t ring, uint16_t (&sc)[kStages], int lane, int t0,
-                                       int t_end, int stride, int lim0, int lim1) {
+                                       int t_end, int stride, const int (&seen_to)[2]) {
   constexpr int kPlane = kTile * (kD / 2);
   const int gid = lane >> 2, tig = lane & 3;
-  lim0 = min(lim0, t_end);
-  lim1 = min(lim1, t_end);
-  float(&shift)[2] = st.shift, (&l_run)[2] = st.l_run, (&o)[8][2][4] = st.o;
-  float m[2] = {-INFINITY, -INFINITY};
-  int e_run = kMinExp;
-  shift[0] = shift[1] = l_run[0] = l_run[1] = 0.0f;
+  float(&shift)[NT] = st.shift, (&l_run)[NT] = st.l_run, (&o)[8][NT][4] = st.o;
+  float m[NT];
+  int lim[NT], e_run = kMinExp;
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    lim[r] = min(seen_to[r], t_end);
+    m[r] = -INFINITY;
+    shift[r] = l_run[r] = 0.0f;
+  }
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.0f;
 
@@ -160,7 +168,7 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
     }
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) sc[i] = sc[i + 1];
-    float s[2][4];  // [row][token 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig]
+    float s[NT][4];  // [row][token 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig]
     {
       uint4 kh[2], kl[2];
 #pragma unroll
@@ -183,37 +191,43 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        s[0][2 * n] = d[n][0];
-        s[0][2 * n + 1] = d[n][1];
-        s[1][2 * n] = d[n][2];
-        s[1][2 * n + 1] = d[n][3];
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+          s[r][2 * n] = d[n][2 * r];
+          s[r][2 * n + 1] = d[n][2 * r + 1];
+        }
       }
     }
-    float vf[4], vmax = 0.0f, tmax[2] = {-INFINITY, -INFINITY};
+    float vf[4], vmax = 0.0f, tmax[NT];
+#pragma unroll
+    for (int r = 0; r < NT; ++r) tmax[r] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
       const float f = half_bits(ks[i]) * (MODE ? 0.0625f * kScale : kScale);
-      // a token that a row does not see counts as -inf whatever its scale holds
-      s[0][i] = t < lim0 ? s[0][i] * f : -INFINITY;
-      s[1][i] = t < lim1 ? s[1][i] * f : -INFINITY;
       vf[i] = half_bits(vs[i]) * (MODE ? 0.0625f : 1.0f);
       vmax = fmaxf(vmax, vf[i]);
-      tmax[0] = fmaxf(tmax[0], s[0][i]);
-      tmax[1] = fmaxf(tmax[1], s[1][i]);
+#pragma unroll
+      for (int r = 0; r < NT; ++r) {
+        // a token that a row does not see counts as -inf whatever its scale holds
+        s[r][i] = t < lim[r] ? s[r][i] * f : -INFINITY;
+        tmax[r] = fmaxf(tmax[r], s[r][i]);
+      }
     }
 #pragma unroll
     for (int x = 1; x <= 2; x <<= 1) {
       vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, x));
-      tmax[0] = fmaxf(tmax[0], __shfl_xor_sync(0xffffffffu, tmax[0], x));
-      tmax[1] = fmaxf(tmax[1], __shfl_xor_sync(0xffffffffu, tmax[1], x));
-    }
-    const int e_tile = vmax > 0.0f ? (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126 : kMinExp;
-    const int e_new = min(100, max(e_run, e_tile));
-    if (__any_sync(0xffffffffu, tmax[0] > m[0] + kSlack || tmax[1] > m[1] + kSlack || e_new > e_run)) {
-      float corr[2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < NT; ++r) tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], x));
+    }
+    bool grown = e_tile_of(vmax) > e_run;
+#pragma unroll
+    for (int r = 0; r < NT; ++r) grown |= tmax[r] > m[r] + kSlack;
+    if (__any_sync(0xffffffffu, grown)) {
+      const int e_new = max(e_run, e_tile_of(vmax));
+      float corr[NT];
+#pragma unroll
+      for (int r = 0; r < NT; ++r) {
         const float old = shift[r];
         const bool fresh = m[r] == -INFINITY;  // a row that has seen no token: nothing to rescale
         if (tmax[r] > m[r] + kSlack) m[r] = tmax[r];
@@ -224,7 +238,7 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
       e_run = e_new;
       // rows 8 nt + 2 tig, + 1 of O^T's columns: their corr is in lanes 8 tig, 8 tig + 4
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
         const float c0 = __shfl_sync(0xffffffffu, corr[nt], 8 * tig);
         const float c1 = __shfl_sync(0xffffffffu, corr[nt], 8 * tig + 4);
 #pragma unroll
@@ -236,9 +250,9 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
         }
       }
     }
-    uint32_t pb[2][2];
+    uint32_t pb[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NT; ++r) {
       float p[4], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -272,7 +286,7 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
           mma_f16(o[2 * h + i][nt], a[0][i], a[1][i], a[2][i], a[3][i], pb[nt][0], pb[nt][1]);
     }
   }
@@ -280,10 +294,11 @@ __device__ __forceinline__ void attend(Part &st, const uint4 *frag, Loader<MODE>
 }
 
 // The state into slot `warp` of the shared memory.
-__device__ __forceinline__ void store_state(State &sh, Part &st, int warp, int lane) {
+template <int NT>
+__device__ __forceinline__ void store_state(State &sh, Part<NT> &st, int warp, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < NT; ++r) {
     st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 1);
     st.l_run[r] += __shfl_xor_sync(0xffffffffu, st.l_run[r], 2);
     if (tig == 0) {
@@ -294,39 +309,38 @@ __device__ __forceinline__ void store_state(State &sh, Part &st, int warp, int l
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
       sh.o[warp][mt][nt][lane] = make_float4(st.o[mt][nt][0], st.o[mt][nt][1], st.o[mt][nt][2], st.o[mt][nt][3]);
 }
 
 // The parts: CTAs below p_ctas take (KV head, row group, part of the prefix),
 // the others (sequence, KV head, row tile, part of its own tokens).
 // part_lse [parts, B L H] (in units of log 2), part_o [parts, B L H, 128].
-template <int MODE>
+template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Plan pl,
                                                             float *__restrict__ part_lse,
                                                             float *__restrict__ part_o) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2;
-  const int64_t H = a.H, rows_out = a.B * a.L * H;
-  const int Hkv = (int)a.Hkv, G = pl.G;
+  const int H = (int)a.H, L = (int)a.L, Hkv = (int)a.Hkv, lgG = pl.lgG;
+  const int64_t rows_out = a.B * a.L * H;
   // Behind the tcgen05 kernel this one does not wait for it: that one began
   // (and let this one begin) when all before it was complete.  Ending after it,
   // as the join needs, is enough.
   if (!pl.tc) griddep_wait();
   griddep_launch_dependents();
-  int64_t cta = blockIdx.x;
+  int cta = blockIdx.x;
   const bool prefix = cta < pl.p_ctas;
-  int j, row0, R, t_begin, t_end, ways, row_warps, part;
-  int64_t bi0, row_base;
+  int j, row0, R, t_begin, t_end, ways, row_warps, part, bi0;
+  int64_t row_base;
   int visible;  // own: tokens that the sequence's query 0 sees
   if (prefix) {
-    const int split = (int)(cta % pl.p_splits);
-    cta /= pl.p_splits;
-    const int group = (int)(cta % pl.p_groups);
-    j = (int)(cta / pl.p_groups);
+    int rest = cta / pl.p_splits;
+    const int split = cta - rest * pl.p_splits;
+    j = rest / pl.p_groups;
     row_warps = pl.row_warps;
-    row0 = group * row_warps * kRows;
-    R = (int)(a.B * a.L) * G;
+    row0 = (rest - j * pl.p_groups) * row_warps * kRows;
+    R = (int)a.B * L << lgG;
     bi0 = 0;
     row_base = j;
     t_begin = split * pl.p_len;
@@ -335,18 +349,17 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
     visible = (int)a.P;
   } else {
     cta -= pl.p_ctas;
-    const int split = (int)(cta % pl.o_splits);
-    cta /= pl.o_splits;
-    const int tile = (int)(cta % pl.o_tiles);
-    cta /= pl.o_tiles;
-    j = (int)(cta % Hkv);
-    const int64_t b = cta / Hkv;
+    int rest = cta / pl.o_splits;
+    const int split = cta - rest * pl.o_splits;
+    int bj = rest / pl.o_tiles;
+    row0 = (rest - bj * pl.o_tiles) * kRows;
+    const int b = bj / Hkv;
+    j = bj - b * Hkv;
     row_warps = 1;
-    row0 = tile * kRows;
-    R = (int)a.L * G;
-    bi0 = b * a.L;
+    R = L << lgG;
+    bi0 = b * L;
     row_base = b * a.cap * Hkv + j;
-    const int len = (int)min((int64_t)a.len[b], a.cap);
+    const int len = min(__ldg(a.len + b), (int)a.cap);
     t_begin = split * pl.o_len;
     if (t_begin >= len) {  // also a sequence that is not taking part: the join reads no such part
       if (pl.tc) griddep_wait();
@@ -354,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
     }
     t_end = min(len, t_begin + pl.o_len);
     part = pl.p_splits + split;
-    visible = len - (int)a.L + 1;
+    visible = len - L + 1;
   }
   ways = kWarps / row_warps;
   const int rw = warp % row_warps, way = warp / row_warps;
   const int r0 = row0 + rw * kRows + gid, r1 = r0 + 8;
-  const int lim0 = r0 >= R ? 0 : prefix ? visible : visible + r0 / G;
-  const int lim1 = r1 >= R ? 0 : prefix ? visible : visible + r1 / G;
+  const int seen_to[2] = {r0 >= R ? 0 : prefix ? visible : visible + (r0 >> lgG),
+                          r1 >= R ? 0 : prefix ? visible : visible + (r1 >> lgG)};
   uint4 *frag = reinterpret_cast<uint4 *>(smem_raw + rw * kFrag);
   uint8_t *rest = smem_raw + row_warps * kFrag;
   const uint32_t ring = smem_u32(rest + warp * kStages * stage_bytes(MODE));
@@ -371,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
   for (int i = 0; i + 1 < kStages; ++i) sc[i] = load(ring + i * stage_bytes(MODE), lane);
   if (way == 0) {
     uint32_t qa[8][4];
-    load_queries(qa, r0 < R ? a.q + query_row(bi0, r0, G, H, j) * kD : nullptr,
-                 r1 < R ? a.q + query_row(bi0, r1, G, H, j) * kD : nullptr, lane & 3);
+    load_queries(qa, r0 < R ? a.q + query_row(bi0, r0, lgG, H, j) * kD : nullptr,
+                 r1 < R ? a.q + query_row(bi0, r1, lgG, H, j) * kD : nullptr, lane & 3);
     // columns 0 2 4 6 1 3 5 7 of each 8, as codes8 gives them: the even ones are
     // k-step 2 w's, the odd ones 2 w + 1's
 #pragma unroll
@@ -387,41 +400,44 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
       }
   }
   __syncthreads();
-  Part st;
-  attend<MODE>(st, frag, load, ring, sc, lane, t0, t_end, stride, lim0, lim1);
+  Part<NT> st;
+  attend<MODE, NT>(st, frag, load, ring, sc, lane, t0, t_end, stride, seen_to);
   __syncthreads();  // the ring's place is free
   State &sh = *reinterpret_cast<State *>(rest);
   store_state(sh, st, warp, lane);
   __syncthreads();
   // the warps' states joined by rows' factors 2^(shift_w - M) / den (0 for a
   // warp that saw no token; NaN scores make l NaN)
-  if (threadIdx.x < row_warps * kRows) {
-    const int w0 = threadIdx.x / kRows, rr = threadIdx.x % kRows, r = row0 + threadIdx.x;
-    float M = -INFINITY, den = 0.0f;
-    for (int w = w0; w < kWarps; w += row_warps)
-      if (sh.l[w][rr] != 0.0f) M = fmaxf(M, sh.m[w][rr]);
-    for (int w = w0; w < kWarps; w += row_warps) {
-      const float l = sh.l[w][rr];
-      const float f = l == 0.0f ? 0.0f : exp2_approx(sh.m[w][rr] - M);
-      den += f * l;
-      sh.m[w][rr] = f;
+  {
+    const int t = threadIdx.x & 127, k = t & (ways - 1), row = t / ways;  // 128 = rows x ways
+    const int w = row / kRows + k * row_warps, rr = row % kRows, r = row0 + row;
+    const bool in = rr < 8 * NT;
+    const float l = in ? sh.l[w][rr] : 0.0f, m = in ? sh.m[w][rr] : 0.0f;
+    float M = l != 0.0f ? m : -INFINITY;
+    for (int x = 1; x < ways; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float f = l == 0.0f ? 0.0f : exp2_approx(m - M);
+    float den = f * l;
+    for (int x = 1; x < ways; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+    __syncwarp();
+    if (threadIdx.x < 128 && in) {
+      sh.m[w][rr] = den == 0.0f ? 0.0f : f / den;
+      if (k == 0 && r < R)
+        part_lse[(int64_t)part * rows_out + query_row(bi0, r, lgG, H, j)] =
+            den == 0.0f ? -INFINITY : M + log2f(den);
     }
-    const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-    for (int w = w0; w < kWarps; w += row_warps) sh.m[w][rr] *= inv;
-    if (r < R)
-      part_lse[(int64_t)part * rows_out + query_row(bi0, r, G, H, j)] =
-          den == 0.0f ? -INFINITY : M + log2f(den);
   }
   __syncthreads();
   // a thread has two rows (8 nt + 2 (lane % 4), + 1) and four columns (16 (lane / 4)
   // + 4 mp ..) of a row tile at a time
-  for (int e = threadIdx.x; e < row_warps * 8 * 32; e += kThreads) {
-    const int l = e & 31, nt = (e >> 5) & 1, mp = (e >> 6) & 3, w0 = e >> 8;
+  for (int e = threadIdx.x; e < row_warps * NT * 4 * 32; e += kThreads) {
+    const int l = e & 31, mp = (e >> 5) & 3, nt = (e >> 7) & (NT - 1), w0 = e / (NT * 128);
     const int rr = 8 * nt + 2 * (l & 3), r0 = row0 + w0 * kRows + rr;
     if (r0 >= R) continue;
     float num[2][4] = {};
-#pragma unroll 4
-    for (int w = w0; w < kWarps; w += row_warps) {
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const int w = w0 + k * row_warps;
+      if (w >= kWarps) break;
       const float4 a4 = sh.o[w][2 * mp][nt][l], b4 = sh.o[w][2 * mp + 1][nt][l];
       const float2 f = *reinterpret_cast<const float2 *>(&sh.m[w][rr]);
       num[0][0] += f.x * a4.x;
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
     for (int i = 0; i < 2; ++i)
       if (r0 + i < R)
         *reinterpret_cast<float4 *>(part_o +
-                                    ((int64_t)part * rows_out + query_row(bi0, r0 + i, G, H, j)) * kD +
+                                    ((int64_t)part * rows_out + query_row(bi0, r0 + i, lgG, H, j)) * kD +
                                     16 * (l >> 2) + 4 * mp) =
             make_float4(num[i][0], num[i][1], num[i][2], num[i][3]);
   }
@@ -448,21 +464,21 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
 __global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, Plan pl,
                                                    const float *__restrict__ part_lse,
                                                    const float *__restrict__ part_o) {
-  const int64_t rows = a.B * a.L * a.H;
-  const int64_t row = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+  const int H = (int)a.H, L = (int)a.L, rows = (int)a.B * L * H;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
   if (row >= rows) return;
-  const int64_t bi = row / a.H;
-  const int h = (int)(row - bi * a.H);
-  const int64_t len = min((int64_t)a.len[bi / a.L], a.cap);
+  const int bi = row / H, h = row - bi * H;
+  const int len = min(a.len[bi / L], (int)a.cap);
   if (len < 0) return;
   // the parts of this row: np of the prefix, then those of its own tokens
   int np = pl.p_splits;
   if (pl.tc)
-    np = tc_parts(pl, (int64_t)(h / pl.G) * pl.tc_groups + (bi * pl.G + h % pl.G) / kTcRows);
-  const int own = pl.o_splits ? (int)((len + pl.o_len - 1) / pl.o_len) : 0;
+    np = tc_parts(pl, (h >> pl.lgG) * pl.tc_groups +
+                          ((bi << pl.lgG) + (h & (pl.G - 1))) / kTcRows);
+  const int own = len > 0 ? (len - 1) / pl.o_len + 1 : 0;
   const int parts = np + own;
   auto slot = [&](int s) { return (int64_t)(s < np ? s : pl.p_splits + s - np) * rows + row; };
   float M = -INFINITY;
@@ -495,49 +511,55 @@ __global__ void __launch_bounds__(256) join_kernel(PrefixAttnArgs a, Plan pl,
   // NaN scores give NaN; a row that sees nothing: zeros
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;
   const uint2 w = make_uint2(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv));
-  reinterpret_cast<uint2 *>(a.out + row * kD)[lane] = w;
+  reinterpret_cast<uint2 *>(a.out + (int64_t)row * kD)[lane] = w;
   if (a.lse && lane == 0)
     a.lse[row] = den == 0.0f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
 }
 
-Plan make_plan(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t cap) {
-  Plan p = {};
+// False where a count is past what the kernels' integers hold.
+bool make_plan(Plan &p, int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P, int64_t cap) {
+  p = {};
   p.G = (int)(H / Hkv);
+  while ((1 << p.lgG) < p.G) ++p.lgG;
+  const int64_t most = 0x3fffffff;
   const int64_t R = B * L * p.G;
-  const int64_t tiles = (R + kRows - 1) / kRows;
-  p.row_warps = tiles >= 8 ? 8 : tiles >= 4 ? 4 : tiles >= 2 ? 2 : 1;
-  p.p_groups = (int)((tiles + p.row_warps - 1) / p.row_warps);
-  const int step = kTile * (kWarps / p.row_warps);  // tokens a CTA takes at a time
   p.tc = P > 0 && R >= kTcMinRows;
   if (p.tc) {
-    p.tc_groups = (int)((R + kTcRows - 1) / kTcRows);
-    p.tc_tiles = (int)((P + kTcTokens - 1) / kTcTokens);
-    p.tc_units = Hkv * p.tc_groups * p.tc_tiles;
+    const int64_t groups = (R + kTcRows - 1) / kTcRows, tiles = (P + kTcTokens - 1) / kTcTokens;
+    const int64_t units = Hkv * groups * tiles;
+    if (units > most) return false;
+    p.tc_groups = (int)groups;
+    p.tc_tiles = (int)tiles;
+    p.tc_units = (int)units;
     // as many CTAs as the longest run of units needs: fewer parts to join, and
     // SMs for the own tokens
-    const int64_t run = (p.tc_units + kSms - 1) / kSms;
-    p.tc_ctas = (int)((p.tc_units + run - 1) / run);
-    for (int64_t item = 0; item < Hkv * p.tc_groups; ++item)
-      p.p_splits = max(p.p_splits, tc_parts(p, item));
-    p.p_groups = 0;
+    p.tc_run = (int)((units + kSms - 1) / kSms);
+    p.tc_ctas = (int)((units + p.tc_run - 1) / p.tc_run);
+    for (int item = 0; item < Hkv * groups; ++item) p.p_splits = max(p.p_splits, tc_parts(p, item));
   } else if (P > 0) {
-    int64_t s = (2 * kSms + Hkv * p.p_groups - 1) / (Hkv * p.p_groups);
-    s = min(s, (P + 4 * step - 1) / (4 * step));
-    s = max((int64_t)1, min(s, (int64_t)64));
+    const int64_t row_tiles = (R + kRows - 1) / kRows;
+    p.row_warps = row_tiles >= 8 ? 8 : row_tiles >= 4 ? 4 : row_tiles >= 2 ? 2 : 1;
+    p.p_groups = (int)((row_tiles + p.row_warps - 1) / p.row_warps);
+    // One CTA an SM with few tokens each, two with more: four tiles a warp.
+    const int64_t step = kTile * (kWarps / p.row_warps), base = Hkv * p.p_groups;
+    int64_t s = max((kSms + base - 1) / base, min((2 * kSms + base - 1) / base, P / (4 * step)));
+    s = max((int64_t)1, min(min(s, (int64_t)64), (P + step - 1) / step));
     p.p_len = (int)(((P + s - 1) / s + step - 1) / step * step);
     p.p_splits = (int)((P + p.p_len - 1) / p.p_len);
+    if (p.p_splits * base > most) return false;
+    p.p_ctas = (int)(p.p_splits * base);
   }
-  p.p_ctas = p.tc ? 0 : (int64_t)p.p_splits * p.p_groups * Hkv;
   p.o_tiles = (int)((L * p.G + kRows - 1) / kRows);
   if (cap > 0) {
-    const int64_t base = B * Hkv * p.o_tiles;
-    int64_t s = max((int64_t)1, (2 * kSms + base - 1) / base);
-    s = min(s, (cap + 255) / 256);
-    p.o_len = (int)(((cap + s - 1) / s + 127) / 128 * 128);
+    const int64_t step = kTile * kWarps, base = B * Hkv * p.o_tiles;
+    int64_t s = max((kSms + base - 1) / base, min((2 * kSms + base - 1) / base, cap / (4 * step)));
+    s = max((int64_t)1, min(s, (cap + step - 1) / step));
+    p.o_len = (int)(((cap + s - 1) / s + step - 1) / step * step);
     p.o_splits = (int)((cap + p.o_len - 1) / p.o_len);
-    p.o_ctas = base * p.o_splits;
+    if (base * p.o_splits > most) return false;
+    p.o_ctas = (int)(base * p.o_splits);
   }
-  return p;
+  return p.p_ctas + p.o_ctas <= most;
 }
 
 }  // namespace pattn
@@ -551,31 +573,36 @@ bool prefix_attention_supported(int64_t B, int64_t L, int64_t H, int64_t Hkv, in
   if (B > lim || L > lim || H > 65535 || P > lim || cap > lim) return false;
   if (B * L > lim / H || B * Hkv > (int64_t)1 << 22) return false;
   if (B == 0) return true;
-  const pattn::Plan p = pattn::make_plan(B, L, H, Hkv, P, cap);
-  return p.p_ctas + p.o_ctas <= 0x7fffffff && p.tc_units <= 0x3fffffff && (B * L * H + 7) / 8 <= 0x7fffffff;
+  pattn::Plan p;
+  return pattn::make_plan(p, B, L, H, Hkv, P, cap);
 }
 
 int64_t prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
                                   int64_t cap) {
   if (B == 0) return 0;
-  const pattn::Plan p = pattn::make_plan(B, L, H, Hkv, P, cap);
+  pattn::Plan p;
+  if (!pattn::make_plan(p, B, L, H, Hkv, P, cap)) return 0;
   const int64_t rows = (int64_t)(p.p_splits + p.o_splits) * B * L * H;
   return (rows + 3) / 4 * 16 + rows * pattn::kD * 4;
 }
 
 cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
-  const pattn::Plan p = pattn::make_plan(a.B, a.L, a.H, a.Hkv, a.P, a.cap);
+  pattn::Plan p;
+  if (!pattn::make_plan(p, a.B, a.L, a.H, a.Hkv, a.P, a.cap)) return cudaErrorInvalidValue;
   const int64_t out_rows = a.B * a.L * a.H;
   const int64_t rows = (int64_t)(p.p_splits + p.o_splits) * out_rows;
   float *lse = static_cast<float *>(a.ws);
   float *o = lse + (rows + 3) / 4 * 4;
-  const int64_t ctas = p.p_ctas + p.o_ctas;
+  const int ctas = p.p_ctas + p.o_ctas;
   if (p.tc) {
     cudaError_t e = pattn::launch_prefix_tc(a, p, lse, o, st);
     if (e != cudaSuccess) return e;
   }
   if (ctas > 0) {
-    auto kern = a.mode ? pattn::parts_kernel<1> : pattn::parts_kernel<0>;
+    // where no CTA has more than 8 rows, its second 8 are left out
+    const int64_t most = (p.p_ctas > 0 ? a.B * a.L : a.L) * p.G;
+    auto kern = most <= 8 ? (a.mode ? pattn::parts_kernel<1, 1> : pattn::parts_kernel<0, 1>)
+                          : (a.mode ? pattn::parts_kernel<1, 2> : pattn::parts_kernel<0, 2>);
     const int smem = pattn::smem_bytes(a.mode, p.p_ctas > 0 ? p.row_warps : 1);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

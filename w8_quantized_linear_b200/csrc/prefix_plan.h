@@ -11,31 +11,28 @@ constexpr int kTcRows = 256, kTcTokens = 128;  // of a unit on the tcgen05 path
 constexpr int64_t kTcMinRows = 64;
 
 struct Plan {
-  int G;                // query heads of a KV head
+  int G, lgG;           // query heads of a KV head, and their logarithm
   // the prefix on the tensor cores' tcgen05 path: units of (256 rows of a KV
-  // head, 128 tokens), dealt to the CTAs in equal runs
+  // head, 128 tokens), dealt to the CTAs in runs
   bool tc;
   int tc_groups;        // row groups of a KV head
   int tc_tiles;         // token tiles of the prefix
-  int64_t tc_units;
-  int tc_ctas;
+  int tc_units, tc_run, tc_ctas;
   // the prefix on mma.sync (few rows): CTAs of (KV head, row group, tokens)
   int row_warps;        // row tiles of a CTA (its other warps split tokens)
-  int p_groups, p_len;
-  int64_t p_ctas;
+  int p_groups, p_len, p_ctas;
   int p_splits;         // parts of a row's prefix, at most
   // own tokens: CTAs of (sequence, KV head, row tile, tokens)
-  int o_tiles, o_splits, o_len;
-  int64_t o_ctas;
+  int o_tiles, o_splits, o_len, o_ctas;
 };
 
-// The CTA that unit u belongs to: CTA c has units floor(c U / n) .. floor((c + 1) U / n) - 1.
-__host__ __device__ inline int64_t tc_cta_of(const Plan &p, int64_t u) {
-  return ((u + 1) * p.tc_ctas - 1) / p.tc_units;
+// Parts of the rows of `item` = KV head * tc_groups + row group: one for each
+// CTA that has units of it (CTA c has units c * tc_run .. (c + 1) * tc_run - 1).
+__host__ __device__ inline int tc_first_cta(const Plan &p, int item) {
+  return item * p.tc_tiles / p.tc_run;
 }
-// Parts of the rows of `item` = KV head * tc_groups + row group.
-__host__ __device__ inline int tc_parts(const Plan &p, int64_t item) {
-  return (int)(tc_cta_of(p, (item + 1) * p.tc_tiles - 1) - tc_cta_of(p, item * p.tc_tiles)) + 1;
+__host__ __device__ inline int tc_parts(const Plan &p, int item) {
+  return ((item + 1) * p.tc_tiles - 1) / p.tc_run - tc_first_cta(p, item) + 1;
 }
 
 cudaError_t launch_prefix_tc(const PrefixAttnArgs &a, const Plan &p, float *part_lse,

@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
            *s_full = q_full + 2, *p_full = s_full + 2, *o_done = p_full + 2, *last_done = o_done + 2;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Hkv = (int)a.Hkv, G = pl.G;
-  const int R = (int)(a.B * a.L) * G;
+  const int Hkv = (int)a.Hkv, lgG = pl.lgG;
+  const int R = (int)(a.B * a.L) << lgG;
   const int64_t rows_out = a.B * a.L * a.H;
 
   if (threadIdx.x == 0) {
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
 
   Units un;
   un.tiles = pl.tc_tiles;
-  un.u = (int)(blockIdx.x * pl.tc_units / pl.tc_ctas);
-  un.end = (int)((blockIdx.x + 1) * pl.tc_units / pl.tc_ctas);
+  un.u = blockIdx.x * pl.tc_run;
+  un.end = min(un.u + pl.tc_run, pl.tc_units);
   int item, t0, n;
 
   if (warp < kSoftmaxWarps) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
       {  // half of a row's query for each thread, in the operand's order
         const int row = first_row + (lane >> 1), r = first + row, half = lane & 1;
         const uint4 *src = reinterpret_cast<const uint4 *>(
-                               a.q + (r < R ? query_row(0, r, G, a.H, j) : 0) * kD) + 8 * half;
+                               a.q + (r < R ? query_row(0, r, lgG, (int)a.H, j) : 0) * kD) + 8 * half;
         uint8_t *dst = sm + kOffQ + x * kOperand + half * (kOperand / 2) + row * 128;
 #pragma unroll 4
         for (int c = 0; c < 8; ++c) {
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
       ok = wait_warp(&o_done[x], (sx - 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const int64_t part = (blockIdx.x - tc_cta_of(pl, (int64_t)item * pl.tc_tiles)) * rows_out;
+      const int64_t part = (int64_t)((int)blockIdx.x - tc_first_cta(pl, item)) * rows_out;
       float inv[2];
       float *dst[2];
 #pragma unroll
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         v += __shfl_xor_sync(0xffffffffu, v, 2);
         inv[r] = 1.0f / v;
         const int row = first + first_row + (lane >> 2) + 8 * r;
-        const int64_t at = part + (row < R ? query_row(0, row, G, a.H, j) : 0);
+        const int64_t at = part + (row < R ? query_row(0, row, lgG, (int)a.H, j) : 0);
         if (row < R && (lane & 3) == 0) part_lse[at] = shift[r] + log2f(v);
         // lane % 4 = 0 .. 3 writes columns 0, 4, 2, 6 and the one behind of each 8
         dst[r] = row < R ? part_o + at * kD + 4 * (lane & 1) + (lane & 2) : nullptr;

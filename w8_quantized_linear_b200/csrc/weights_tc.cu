@@ -85,7 +85,7 @@ struct Run {  // a CTA's run of tiles
 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
-    const __grid_constant__ CUtensorMap tm_q, KvWeightsArgs a, int G) {
+    const __grid_constant__ CUtensorMap tm_q, KvWeightsArgs a, int lgG) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + (-smem_u32(smem_raw) & 1023u);
   float *sets = reinterpret_cast<float *>(sm + kOffSet);
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
            *k_free = k_full + 2, *last_done = k_free + 2;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Hkv = (int)a.Hkv, cap = (int)a.cap, R = (int)(a.B * a.L) * G;
+  const int Hkv = (int)a.Hkv, cap = (int)a.cap, G = 1 << lgG, R = (int)(a.B * a.L) << lgG;
   const int row_tiles = (R + kTile - 1) / kTile;
 
   if (threadIdx.x == 0) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(
         for (int n = 0; n < 4; ++n) {
           const int c = 32 * n + lane, r = i * kTile + c;
           // a row without weight (lse -inf), or behind the last, gives none
-          const float e = r < R ? __ldg(a.lse + query_row(0, r, G, a.H, sg.j)) : -INFINITY;
+          const float e = r < R ? __ldg(a.lse + query_row(0, r, lgG, (int)a.H, sg.j)) : -INFINITY;
           sets[set * kSet + ((c >> 1) & 3) * kSetRow + 2 * (c >> 3) + (c & 1)] =
               e == -INFINITY ? -INFINITY : -e * kLog2e;
         }
@@ -360,6 +360,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 cudaError_t launch_weights_tc(const KvWeightsArgs &a, cudaStream_t st) {
   const int64_t tiles = a.Hkv * ((a.cap + kTile - 1) / kTile);
   const int G = (int)(a.H / a.Hkv);
+  int lgG = 0;
+  while ((1 << lgG) < G) ++lgG;
   // q [B L, H, 128]: a row tile is 128 / G queries of one KV head's G heads, in
   // two halves of 64 columns
   auto fn = encode_fn();
@@ -376,7 +378,7 @@ cudaError_t launch_weights_tc(const KvWeightsArgs &a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)(tiles < kSms ? tiles : kSms)), dim3(kThreads), kSmem, st,
-                    true, tm, a, G);
+                    true, tm, a, lgG);
 }
 
 }  // namespace evict

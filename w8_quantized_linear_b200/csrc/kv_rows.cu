@@ -11,6 +11,7 @@
 // themselves.  The top 32 bits become the argument of sincospif in [-1, 1).
 #include "common.cuh"
 #include "launch.h"
+#include "nested_mma.cuh"
 
 namespace bitnest {
 
@@ -227,11 +228,24 @@ cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
 constexpr int kD = 128;
 constexpr int kRowLanes = 16;
 
-// max |v| over the 16 lanes of a row
-__device__ __forceinline__ float row_max(float m) {
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The low nibbles of eight words as the eight nibbles of one.
+__device__ __forceinline__ uint32_t nibbles8(const uint32_t (&w)[8]) {
+  uint32_t half[2];
 #pragma unroll
-  for (int o = kRowLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = prmt(prmt(w[4 * h], w[4 * h + 1], 0x0040), prmt(w[4 * h + 2], w[4 * h + 3], 0x0040), 0x5410);
+    half[h] = (x & 0x000F000Fu) | ((x >> 4) & 0x00F000F0u);  // bytes 0 and 2
+  }
+  return prmt(half[0], half[1], 0x6420);
 }
 
 // The packer's rule on 8 values of a row that are exact in fp16 (see
@@ -240,165 +254,221 @@ __device__ __forceinline__ float row_max(float m) {
 // unless s is subnormal in fp16 and was rounded down; then q is clamped to
 // -8 .. 7 as well.
 //
-// The division is done as RN(x RN(1 / s)): where |t| <= 7.25 that is within
-// 1.1e-6 of x / s and RN(x / s) within 2.4e-7, so 16 t is known to 2.2e-5 and
-// both nibbles are the same unless 16 t lies within 2^-15 of a half-integer
-// (r) or of 8 mod 16 (q); only such a value pays for the divisions.
+// The division is done as x rcp(s), rcp off by 2^-23 at most: where |t| <= 7.25
+// that is within 1.1e-6 of x / s and RN(x / s) within 2.4e-7, so 16 t is known
+// to 2.2e-5 and both nibbles are the same unless 16 t lies within 2^-15 of a
+// half-integer (r) or of 8 mod 16 (q); only such a value pays for the division.
+// Adding 1.5 * 2^23 rounds to an integer, 1.5 * 2^27 to a multiple of 16, whose
+// two's complement is in the low bits; the codes' offset 8 flips a nibble's top
+// bit.
 __device__ __forceinline__ void pack8(const float (&x)[8], float m, float s, uint32_t &hi,
                                       uint32_t &lo) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+  constexpr float kInt = 12582912.0f, kSixteen = 201326592.0f;  // 1.5 * 2^23, 1.5 * 2^27
   constexpr float kNear = 3.0517578125e-05f;
-  const float rs = s == 0.0f ? 0.0f : __frcp_rn(s);
-  hi = lo = 0;
-  bool near = m * rs > 7.25f;
+  const float rs = s == 0.0f ? 0.0f : rcp_approx(s) * 16.0f;
   uint32_t qb[8], rb[8];
+  float far_r = 0.0f, far_q = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fmul_rn(x[i], rs);
-    const float q = __fsub_rn(__fadd_rn(t, kRound), kRound);
-    const float u = __fmul_rn(16.0f, __fsub_rn(t, q));  // exact, |u| <= 8
-    const float ur = __fadd_rn(u, kRound);
-    const float r = __fsub_rn(ur, kRound);
-    near |= fabsf(__fsub_rn(u, r)) > 0.5f - kNear || fabsf(u) > 8.0f - kNear;
-    qb[i] = __float_as_uint(__fadd_rn(q, kRound + 8.0f));
-    rb[i] = __float_as_uint(__fadd_rn(fminf(r, 7.0f), kRound + 8.0f));
+  for (int i = 0; i < 8; i += 2) {
+    float t[2], q[2], u[2], r[2];
+    f32x2_mul(t[0], t[1], x[i], x[i + 1], rs, rs);  // 16 t
+    f32x2_add(q[0], q[1], t[0], t[1], kSixteen, kSixteen);
+    qb[i] = __float_as_uint(q[0]);
+    qb[i + 1] = __float_as_uint(q[1]);
+    f32x2_sub(q[0], q[1], q[0], q[1], kSixteen, kSixteen);
+    f32x2_sub(u[0], u[1], t[0], t[1], q[0], q[1]);  // exact, |u| <= 8
+    f32x2_add(r[0], r[1], u[0], u[1], kInt, kInt);
+    rb[i] = __float_as_uint(fminf(r[0], kInt + 7.0f));
+    rb[i + 1] = __float_as_uint(fminf(r[1], kInt + 7.0f));
+    f32x2_sub(r[0], r[1], r[0], r[1], kInt, kInt);
+    f32x2_sub(r[0], r[1], u[0], u[1], r[0], r[1]);
+    far_r = max3_abs(far_r, r[0], r[1]);
+    far_q = max3_abs(far_q, u[0], u[1]);
   }
-  if (near) {
-#pragma unroll
+  const bool wide = m * rs > 16.0f * 7.25f;
+  if (far_r > 0.5f - kNear || far_q > 8.0f - kNear || wide) {
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
-      float q = 0.0f, r = 0.0f;
-      if (s != 0.0f) {
-        const float t = __fdiv_rn(x[i], s);
-        q = fmaxf(-8.0f, fminf(7.0f, rintf(t)));
-        r = fmaxf(-8.0f, fminf(7.0f, rintf(__fmul_rn(16.0f, __fsub_rn(t, q)))));
-      }
-      qb[i] = __float_as_uint(__fadd_rn(q, kRound + 8.0f));
-      rb[i] = __float_as_uint(__fadd_rn(r, kRound + 8.0f));
+      float v = 0.0f;  // x[i], without an index into registers
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v = k == i ? x[k] : v;
+      const float t16 = v * rs, u = t16 - ((t16 + kSixteen) - kSixteen), d = u - ((u + kInt) - kInt);
+      if (!(wide || fabsf(d) > 0.5f - kNear || fabsf(u) > 8.0f - kNear)) continue;
+      const float t = __fdiv_rn(v, s);  // s > 0: t16 is 0 otherwise
+      const float q = fmaxf(-8.0f, fminf(7.0f, rintf(t)));
+      const float r = fmaxf(-8.0f, fminf(7.0f, rintf(__fmul_rn(16.0f, __fsub_rn(t, q)))));
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k == i) {
+          qb[k] = __float_as_uint(__fadd_rn(q, kInt));
+          rb[k] = __float_as_uint(__fadd_rn(r, kInt));
+        }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {  // column i in nibble i: byte i / 2, low nibble first
-    hi |= (qb[i] & 15u) << (4 * i);
-    lo |= (rb[i] & 15u) << (4 * i);
-  }
+  hi = nibbles8(qb) ^ 0x88888888u;  // column i in nibble i: byte i / 2, low nibble first
+  lo = nibbles8(rb) ^ 0x88888888u;
 }
 
 __device__ __forceinline__ void round_half8(float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __half2float(__float2half_rn(v[i]));
+  for (int i = 0; i < 8; i += 2) {
+    const float2 f = __half22float2(__floats2half2_rn(v[i], v[i + 1]));
+    v[i] = f.x;
+    v[i + 1] = f.y;
+  }
 }
 
-// One 16-lane group per (token, `per` heads), blockIdx.y = 0: keys, 1: values.
+// One 16-lane group per token (of 16 in a block) and `per` heads (blockIdx.z);
+// blockIdx.y = 0: keys, 1: values.  A lane has two runs of four columns, at c0
+// and c1: the two of its four pairs in the halves layout, neighbours elsewhere.
+// A batch of heads is loaded together.
+//
+// Bound: instructions (16384 x 8 fp16 rows are 101 MB, 15 us to move): hence
+// packed arithmetic, nibbles gathered by byte permutations, one reciprocal a
+// row, and 32-bit indexes up to the row's.
+constexpr int kBatch = 4;
 template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a, int per) {
   const int lane = threadIdx.x & (kRowLanes - 1);
-  const int64_t id = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / kRowLanes;
-  const int groups = ((int)a.Hkv + per - 1) / per;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t token = id / groups;  // b * L + i
+  const uint32_t token = blockIdx.x * 16u + threadIdx.x / kRowLanes;  // b * L + i
   const bool values = blockIdx.y != 0;
   // whole warps run on: the shuffles below need every lane
-  bool live = token < a.B * a.L;
+  bool live = token < (uint32_t)(a.B * a.L);
   int64_t row0 = 0;
   if (live) {
-    const int64_t b = token / a.L, i = token - b * a.L;
+    const uint32_t b = token / (uint32_t)a.L, i = token - b * (uint32_t)a.L;
     const int64_t t = (int64_t)a.start[b] + i;
-    live = t >= 0 && t < a.cap && (!a.count || i < a.count[b]);
+    live = t >= 0 && t < a.cap && (!a.count || (int)i < a.count[b]);
     row0 = (b * a.cap + t) * a.Hkv;
   }
-  const int hg = (int)(id - token * groups);
-  float c[8], s[8];
-  const bool turning = !values && a.phase != nullptr && 8 * lane < a.rot;
-  const int half_lanes = (int)a.rot / 16;  // lanes of a half of the turned values
+  const int hg = blockIdx.z;
+  const int rot = values || !a.phase ? 0 : (int)a.rot;
+  const bool turning = 8 * lane < rot;
+  const bool apart = !PAIRS && turning;
+  const int c0 = apart ? 4 * lane : 8 * lane, c1 = apart ? rot / 2 + 4 * lane : 8 * lane + 4;
+  float c[4], s[4];
   if (turning && live) {
     const int32_t p = a.pos[token];
 #pragma unroll
-    for (int i = 0; i < (PAIRS ? 4 : 8); ++i) {
-      const int pair = PAIRS ? 4 * lane + i : 8 * (lane < half_lanes ? lane : lane - half_lanes) + i;
-      turn(a.phase[pair], p, 1.0f, a.mag, c[i], s[i]);
-    }
+    for (int i = 0; i < 4; ++i) turn(a.phase[4 * lane + i], p, 1.0f, a.mag, c[i], s[i]);
   }
   const T *src = static_cast<const T *>(values ? a.v : a.k) +
-                 (live ? token * (values ? a.v_token : a.k_token) : 0) + 8 * lane;
+                 (live ? token * (values ? a.v_token : a.k_token) : 0);
   uint8_t *hi = values ? a.cache.v_hi : a.cache.k_hi;
   uint8_t *lo = values ? a.cache.v_lo : a.cache.k_lo;
   uint16_t *sc = values ? a.cache.v_scale : a.cache.k_scale;
-  for (int n = 0; n < per; ++n) {
-    const int j = hg * per + n;
-    const bool ok = live && j < a.Hkv;
-    float v[8] = {};
-    if (ok) load_vec<T, 8>(src + (int64_t)j * kD, v);
-    if (a.phase != nullptr && !values) {  // the same for the whole block
-      if constexpr (PAIRS) {
-        if (turning)
+  const int h_end = min((int)a.Hkv, (hg + 1) * per);
+  for (int h = hg * per; h < h_end; h += kBatch) {
+    float v[kBatch][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = v[2 * i], y = v[2 * i + 1];
-            v[2 * i] = x * c[i] - y * s[i];
-            v[2 * i + 1] = x * s[i] + y * c[i];
-          }
+    for (int n = 0; n < kBatch; ++n) {
+      if (live && h + n < h_end) {
+        const T *p = src + (int64_t)(h + n) * kD;
+        float x[4], y[4];
+        load_vec<T, 4>(p + c0, x);
+        load_vec<T, 4>(p + c1, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[n][i] = x[i], v[n][4 + i] = y[i];
       } else {
-        // the other of each pair sits half_lanes further
-        const int other = (threadIdx.x & 16) |
-                          (lane < half_lanes ? lane + half_lanes : turning ? lane - half_lanes : lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float w = __shfl_sync(0xffffffffu, v[i], other);
-          if (turning) v[i] = lane < half_lanes ? v[i] * c[i] - w * s[i] : w * s[i] + v[i] * c[i];
-        }
+        for (int i = 0; i < 8; ++i) v[n][i] = 0.0f;
       }
     }
-    // to fp16 first, as bitnest_rope's output is: the same bits as turning and
-    // packing in two calls
-    round_half8(v);
-    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-    m = row_max(m);
-    const __half sh = __float2half_rn(__fdiv_rn(m, 7.0f));
-    uint32_t h4, l4;
-    pack8(v, m, __half2float(sh), h4, l4);
-    if (ok) {
-      const int64_t row = row0 + j;
-      reinterpret_cast<uint32_t *>(hi + row * (kD / 2))[lane] = h4;
-      reinterpret_cast<uint32_t *>(lo + row * (kD / 2))[lane] = l4;
-      if (lane == 0) sc[row] = __half_as_ushort(sh);
+    for (int n = 0; n < kBatch; ++n) {
+      float(&x)[8] = v[n];
+      if (turning)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float &p = x[PAIRS ? 2 * i : i], &q = x[PAIRS ? 2 * i + 1 : 4 + i];
+          const float t = p * c[i] - q * s[i];
+          q = p * s[i] + q * c[i];
+          p = t;
+        }
+      // to fp16 first, as bitnest_rope's output is: the same bits as turning and
+      // packing in two calls
+      if (sizeof(T) == 4 || turning) round_half8(x);
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) m = max3_abs(m, x[i], x[i + 1]);
+#pragma unroll
+      for (int o = kRowLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // fp16(m / 7): m / 7 is never within 2^-4 steps of the middle of two fp16
+      // values (7 (2 k + 1) is odd), the product within 2^-23 of it
+      const __half sh = __float2half_rn(m * 0.14285714285714286f);
+      uint32_t h4, l4;
+      pack8(x, m, __half2float(sh), h4, l4);
+      if (live && h + n < h_end) {
+        const int64_t row = row0 + h + n;
+        uint8_t *ph = hi + row * (kD / 2), *pl = lo + row * (kD / 2);
+        if (apart) {
+          *reinterpret_cast<uint16_t *>(ph + c0 / 2) = (uint16_t)h4;
+          *reinterpret_cast<uint16_t *>(ph + c1 / 2) = (uint16_t)(h4 >> 16);
+          *reinterpret_cast<uint16_t *>(pl + c0 / 2) = (uint16_t)l4;
+          *reinterpret_cast<uint16_t *>(pl + c1 / 2) = (uint16_t)(l4 >> 16);
+        } else {
+          *reinterpret_cast<uint32_t *>(ph + c0 / 2) = h4;
+          *reinterpret_cast<uint32_t *>(pl + c0 / 2) = l4;
+        }
+        if (lane == 0) sc[row] = __half_as_ushort(sh);
+      }
     }
   }
 }
 
-// 16 lanes a row, 8 values (4 bytes of each plane) a lane; blockIdx.y as above.
+// 16 lanes a row, 8 values (4 bytes of each plane) a lane; a token (of 16 in a
+// block) and four heads (blockIdx.z) a thread; blockIdx.y as above.  The codes
+// are exact in fp16 (in sixteenths for the target), so one fp16 product with
+// the scale rounds once.
+constexpr int kReadRows = 4;
 template <int MODE>
 __global__ void __launch_bounds__(256) kv_read_kernel(ReadArgs a) {
   const int lane = threadIdx.x & (kRowLanes - 1);
-  const int64_t id = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / kRowLanes;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t token = id / a.Hkv;
-  if (token >= a.B * a.L) return;
-  const int64_t b = token / a.L, i = token - b * a.L;
-  const int64_t t = (a.start ? (int64_t)a.start[b] : 0) + i;
+  const uint32_t token = blockIdx.x * 16u + threadIdx.x / kRowLanes;
+  if (token >= (uint32_t)(a.B * a.L)) return;
+  const uint32_t b = token / (uint32_t)a.L;
+  const int64_t t = (a.start ? (int64_t)a.start[b] : 0) + (token - b * (uint32_t)a.L);
+  const bool in = t >= 0 && t < a.cap;  // rows outside the cache read as zeros
   const bool values = blockIdx.y != 0;
-  uint16_t *out = (values ? a.v : a.k) + id * kD + 8 * lane;
-  float v[8] = {};
-  if (t >= 0 && t < a.cap) {  // rows outside the cache read as zeros
-    const int64_t row = (b * a.cap + t) * a.Hkv + (id - token * a.Hkv);
-    const uint32_t h =
-        reinterpret_cast<const uint32_t *>((values ? a.cache.v_hi : a.cache.k_hi) + row * (kD / 2))[lane];
-    uint32_t l = 0;
-    if (MODE)
-      l = reinterpret_cast<const uint32_t *>((values ? a.cache.v_lo : a.cache.k_lo) + row * (kD / 2))[lane];
-    float s = __half2float(__ushort_as_half((values ? a.cache.v_scale : a.cache.k_scale)[row]));
-    if (MODE) s *= 0.0625f;
+  const int j0 = blockIdx.z * kReadRows, heads = min((int)a.Hkv - j0, kReadRows);
+  const int64_t row = (b * a.cap + t) * a.Hkv + j0;
+  const uint32_t *hi = reinterpret_cast<const uint32_t *>((values ? a.cache.v_hi : a.cache.k_hi) + row * (kD / 2)) + lane;
+  const uint32_t *lo = reinterpret_cast<const uint32_t *>((values ? a.cache.v_lo : a.cache.k_lo) + row * (kD / 2)) + lane;
+  const uint16_t *sc = (values ? a.cache.v_scale : a.cache.k_scale) + row;
+  uint4 *out = reinterpret_cast<uint4 *>((values ? a.v : a.k) + ((int64_t)token * a.Hkv + j0) * kD) + lane;
+  uint32_t h[kReadRows], l[kReadRows];
+  uint16_t s[kReadRows];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int q = (int)((h >> (4 * c)) & 15u);
-      const int u = MODE ? 16 * q + (int)((l >> (4 * c)) & 15u) - 136 : q - 8;
-      v[c] = (float)u * s;
+  for (int n = 0; n < kReadRows; ++n) {
+    h[n] = l[n] = 0x88888888u;
+    s[n] = 0;
+    if (in && n < heads) {
+      h[n] = hi[n * (kD / 8)];
+      if (MODE) l[n] = lo[n * (kD / 8)];
+      s[n] = sc[n];
     }
   }
-  store_vec<__half, 8>(reinterpret_cast<__half *>(out), v);
+#pragma unroll
+  for (int n = 0; n < kReadRows; ++n) {
+    if (n >= heads) break;
+    uint32_t ev, od, w[4];
+    nested::codes<MODE>(h[n], l[n], ev, od);
+    const __half2 scale = __half2half2(__ushort_as_half(s[n]));
+    // 0x6400 | u is 1024 + u: times 1/16 and less (1024 + 136) / 16, exact
+    const __half2 unit = __float2half2_rn(MODE ? 0.0625f : 1.0f);
+    const __half2 offset = __float2half2_rn(MODE ? -72.5f : -1032.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = (prmt(ev, od, (uint32_t)i | ((uint32_t)(i + 4) << 8)) & 0x00FF00FFu) | 0x64006400u;
+      const __half2 v = __hmul2(__hfma2(*reinterpret_cast<const __half2 *>(&u), unit, offset), scale);
+      w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    out[n * (kD / 8)] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 }  // namespace rows
@@ -413,15 +483,14 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st) {
 
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t st) {
   // Heads that a 16-lane group goes over with one set of cosines and sines:
-  // as many as leave four blocks for each SM, at most 8.
+  // as many as leave four blocks for each SM, at most 8, and at least what the
+  // grid's third dimension asks for.
+  const int64_t blocks = (a.B * a.L + 15) / 16;
   int per = 1;
-  while (per < 8 && per < a.Hkv &&
-         2 * a.B * a.L * ((a.Hkv + 2 * per - 1) / (2 * per)) * rows::kRowLanes >= 4 * 148 * 256)
+  while (per < a.Hkv && ((per < 8 && 2 * blocks * ((a.Hkv + 2 * per - 1) / (2 * per)) >= 4 * 148) ||
+                         (a.Hkv + per - 1) / per > 65535))
     per *= 2;
-  const int64_t threads = a.B * a.L * ((a.Hkv + per - 1) / per) * rows::kRowLanes;
-  const int64_t blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks, 2);
+  const dim3 grid((unsigned)blocks, 2, (unsigned)((a.Hkv + per - 1) / per));
   auto kern = a.type == 0 ? (a.pairs ? rows::kv_append_kernel<__half, true>
                                      : rows::kv_append_kernel<__half, false>)
                           : (a.pairs ? rows::kv_append_kernel<float, true>
@@ -430,10 +499,10 @@ cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t st) {
-  const int64_t blocks = (a.B * a.L * a.Hkv * rows::kRowLanes + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((a.B * a.L + 15) / 16), 2,
+                  (unsigned)((a.Hkv + rows::kReadRows - 1) / rows::kReadRows));
   auto kern = a.mode ? rows::kv_read_kernel<1> : rows::kv_read_kernel<0>;
-  return launch_pdl(kern, dim3((unsigned)blocks, 2), dim3(256), 0, st, true, a);
+  return launch_pdl(kern, grid, dim3(256), 0, st, true, a);
 }
 
 }  // namespace bitnest

@@ -254,55 +254,45 @@ __device__ __forceinline__ uint32_t nibbles8(const uint32_t (&w)[8]) {
 // unless s is subnormal in fp16 and was rounded down; then q is clamped to
 // -8 .. 7 as well.
 //
-// The division is done as x rcp(s), rcp off by 2^-23 at most: where |t| <= 7.25
-// that is within 1.1e-6 of x / s and RN(x / s) within 2.4e-7, so 16 t is known
-// to 2.2e-5 and both nibbles are the same unless 16 t lies within 2^-15 of a
-// half-integer (r) or of 8 mod 16 (q); only such a value pays for the division.
+// No division: T = 16 t is x 16 rcp(s), rounded to a multiple of 2^-13.  With
+// x = X 2^a, s = S 2^b (X, S integers below 2^11) the exact T is off a half
+// integer, where a rounding changes, by |32 X 2^(a-b) - (2 k + 1) S| / 2 S: by
+// nothing or by 1 / 2 S > 2.4e-4 at least (for a - b < -5 as well: T <= 1/2
+// then, and X < 2 S).  rcp is off by 2^-23 at most, so where |t| <= 7.25 the
+// product is off by 2.2e-5: the rounding to 2^-13 gives the half integers
+// exactly, and moves nothing else across one or onto one.
 // Adding 1.5 * 2^23 rounds to an integer, 1.5 * 2^27 to a multiple of 16, whose
 // two's complement is in the low bits; the codes' offset 8 flips a nibble's top
 // bit.
 __device__ __forceinline__ void pack8(const float (&x)[8], float m, float s, uint32_t &hi,
                                       uint32_t &lo) {
   constexpr float kInt = 12582912.0f, kSixteen = 201326592.0f;  // 1.5 * 2^23, 1.5 * 2^27
-  constexpr float kNear = 3.0517578125e-05f;
+  constexpr float kGrid = 1536.0f;                              // 1.5 * 2^10: to 2^-13
   const float rs = s == 0.0f ? 0.0f : rcp_approx(s) * 16.0f;
   uint32_t qb[8], rb[8];
-  float far_r = 0.0f, far_q = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
-    float t[2], q[2], u[2], r[2];
-    f32x2_mul(t[0], t[1], x[i], x[i + 1], rs, rs);  // 16 t
+    float t[2], q[2], u[2];
+    f32x2_mul(t[0], t[1], x[i], x[i + 1], rs, rs);
+    f32x2_add(t[0], t[1], t[0], t[1], kGrid, kGrid);
+    f32x2_sub(t[0], t[1], t[0], t[1], kGrid, kGrid);
     f32x2_add(q[0], q[1], t[0], t[1], kSixteen, kSixteen);
     qb[i] = __float_as_uint(q[0]);
     qb[i + 1] = __float_as_uint(q[1]);
     f32x2_sub(q[0], q[1], q[0], q[1], kSixteen, kSixteen);
     f32x2_sub(u[0], u[1], t[0], t[1], q[0], q[1]);  // exact, |u| <= 8
-    f32x2_add(r[0], r[1], u[0], u[1], kInt, kInt);
-    rb[i] = __float_as_uint(fminf(r[0], kInt + 7.0f));
-    rb[i + 1] = __float_as_uint(fminf(r[1], kInt + 7.0f));
-    f32x2_sub(r[0], r[1], r[0], r[1], kInt, kInt);
-    f32x2_sub(r[0], r[1], u[0], u[1], r[0], r[1]);
-    far_r = max3_abs(far_r, r[0], r[1]);
-    far_q = max3_abs(far_q, u[0], u[1]);
+    f32x2_add(u[0], u[1], u[0], u[1], kInt, kInt);
+    rb[i] = __float_as_uint(fminf(u[0], kInt + 7.0f));
+    rb[i + 1] = __float_as_uint(fminf(u[1], kInt + 7.0f));
   }
-  const bool wide = m * rs > 16.0f * 7.25f;
-  if (far_r > 0.5f - kNear || far_q > 8.0f - kNear || wide) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      float v = 0.0f;  // x[i], without an index into registers
+  if (m * rs > 16.0f * 7.25f) {  // a subnormal scale
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v = k == i ? x[k] : v;
-      const float t16 = v * rs, u = t16 - ((t16 + kSixteen) - kSixteen), d = u - ((u + kInt) - kInt);
-      if (!(wide || fabsf(d) > 0.5f - kNear || fabsf(u) > 8.0f - kNear)) continue;
-      const float t = __fdiv_rn(v, s);  // s > 0: t16 is 0 otherwise
+    for (int i = 0; i < 8; ++i) {
+      const float t = __fdiv_rn(x[i], s);
       const float q = fmaxf(-8.0f, fminf(7.0f, rintf(t)));
       const float r = fmaxf(-8.0f, fminf(7.0f, rintf(__fmul_rn(16.0f, __fsub_rn(t, q)))));
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k == i) {
-          qb[k] = __float_as_uint(__fadd_rn(q, kInt));
-          rb[k] = __float_as_uint(__fadd_rn(r, kInt));
-        }
+      qb[i] = __float_as_uint(__fadd_rn(q, kInt));
+      rb[i] = __float_as_uint(__fadd_rn(r, kInt));
     }
   }
   hi = nibbles8(qb) ^ 0x88888888u;  // column i in nibble i: byte i / 2, low nibble first

@@ -1,7 +1,10 @@
 // A bounded nested KV cache: the attention weight each cached token has
 // received, and eviction of the tokens that received least.
+#include <algorithm>
+
 #include "launch.h"
 #include "nested_mma.cuh"
+#include "sm100.cuh"
 
 namespace bitnest {
 
@@ -117,6 +120,145 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
     for (int w = 0; w < ways; ++w) v += part[(e / kTokens) * ways + w][e % kTokens];
     a.acc[(b * a.Hkv + j) * a.cap + t] += v;
   }
+}
+
+// The same where a cache's rows are at most 128 (each sequence's own tokens
+// mostly, and a shared prefix of a small batch): the rows' queries are held as A fragments in shared memory, and each warp brings
+// 16 tokens at a time through a ring of asynchronous copies, so that the K
+// planes stream in beside the products.  A CTA takes a part of one (cache,
+// KV head)'s tokens; a token belongs to one warp, its sum to a fixed order.
+constexpr int kOwnTile = 16, kStages = 3, kMostTiles = 8;
+template <int MODE>
+__global__ void __launch_bounds__(kWarps * 32, 3) few_rows_kernel(KvWeightsArgs a, int lgG, int splits,
+                                                                     int part_len) {
+  constexpr int kPlane = kOwnTile * (kD / 2), kStage = (MODE ? 2 : 1) * kPlane;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float base[kMostTiles * 16];  // -lse log2(e) of the rows, -inf for one without weight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const bool own = a.len != nullptr;  // else one cache, which every query sees whole
+  const int Hkv = (int)a.Hkv, L = (int)(own ? a.L : a.B * a.L);
+  const int R = L << lgG, row_tiles = (R + 15) / 16;
+  const int bj = blockIdx.x / splits, split = blockIdx.x - bj * splits;
+  const int b = bj / Hkv, j = bj - b * Hkv, bi0 = b * L;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int len = own ? min(a.len[b], (int)a.cap) : (int)a.cap;
+  const int t_begin = split * part_len;
+  if (t_begin >= len) return;
+  const int t_end = min(len, t_begin + part_len);
+  uint4 *frag = reinterpret_cast<uint4 *>(smem);
+  const uint32_t ring = smem_u32(smem + row_tiles * kFrag + warp * kStages * kStage);
+
+  // this lane's copies: pieces lane % 4 of rows lane / 4 and 8 + lane / 4; lane
+  // l < 16 has token l's scale and sum so far
+  const int64_t row_base = b * a.cap * Hkv + j;
+  int t0 = t_begin + warp * kOwnTile;
+  constexpr int kStep = kWarps * kOwnTile;
+  const int64_t next = (int64_t)kStep * Hkv * (kD / 2), half = (int64_t)8 * Hkv * (kD / 2);
+  int64_t off = (row_base + (int64_t)(t0 + gid) * Hkv) * (kD / 2) + 16 * tig;
+  int t_load = t0;
+  float *const acc = a.acc + (int64_t)bj * a.cap;
+  auto load = [&](uint32_t at, uint16_t &scale, float &old) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const bool in = t_load + gid + 8 * n < t_end;
+      const int64_t o = in ? off + n * half : 0;
+      cp_async16(at + (gid + 8 * n) * (kD / 2) + 16 * tig, a.k_hi + o, in);
+      if (MODE) cp_async16(at + kPlane + (gid + 8 * n) * (kD / 2) + 16 * tig, a.k_lo + o, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int t = t_load + (lane & 15);
+    const bool in = t < t_end;
+    scale = in ? __ldg(a.k_scale + row_base + (int64_t)t * Hkv) : (uint16_t)0;
+    old = in ? acc[t] : 0.0f;
+    off += next;
+    t_load += kStep;
+  };
+  uint16_t sc[kStages];
+  float old[kStages];
+#pragma unroll
+  for (int i = 0; i + 1 < kStages; ++i) load(ring + i * kStage, sc[i], old[i]);
+  for (int r = warp; r < row_tiles; r += kWarps) {
+    const int r0 = 16 * r + gid, r1 = r0 + 8;
+    uint32_t qa[8][4];
+    load_queries(qa, r0 < R ? a.q + query_row(bi0, r0, lgG, (int)a.H, j) * kD : nullptr,
+                 r1 < R ? a.q + query_row(bi0, r1, lgG, (int)a.H, j) * kD : nullptr, tig);
+    store_frag(frag + r * (kFrag / 16), qa, lane);
+  }
+  for (int r = threadIdx.x; r < 16 * row_tiles; r += kWarps * 32) {
+    const float e = r < R ? a.lse[query_row(bi0, r, lgG, (int)a.H, j)] : -INFINITY;
+    base[r] = e == -INFINITY ? -INFINITY : -e * kLog2e;
+  }
+  __syncthreads();
+
+  for (int slot = 0; t0 < t_end; t0 += kStep) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // this tile is here, and every lane is done with the one before
+    const int free = slot == 0 ? kStages - 1 : slot - 1;
+    load(ring + free * kStage, sc[kStages - 1], old[kStages - 1]);
+    const uint32_t cur = ring + slot * kStage;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    float f[4], sum[4] = {};  // tokens 2 tig, 2 tig + 1, 8 + 2 tig, 9 + 2 tig
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 2 * tig + (i & 1) + 8 * (i >> 1);
+      f[i] = half_bits((uint16_t)__shfl_sync(0xffffffffu, (int)sc[0], t)) * (MODE ? 0.0625f * kScale : kScale);
+    }
+    const float before = old[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) {
+      sc[i] = sc[i + 1];
+      old[i] = old[i + 1];
+    }
+    uint4 u[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint4 h = lds128(cur + (8 * n + gid) * (kD / 2) + 16 * tig);
+      const uint4 l = MODE ? lds128(cur + kPlane + (8 * n + gid) * (kD / 2) + 16 * tig) : make_uint4(0, 0, 0, 0);
+      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) u[n][w] = codes8<MODE>(hw[w], lw[w]);
+    }
+    const bool edge = own && t0 + kOwnTile > len - L + 1;  // some row does not see some token
+    for (int r = 0; r < row_tiles; ++r) {
+      float d[2][4] = {};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint4 q0 = frag[r * (kFrag / 16) + (2 * w) * 32 + lane],
+                    q1 = frag[r * (kFrag / 16) + (2 * w + 1) * 32 + lane];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          mma_f16(d[n], q0.x, q0.y, q0.z, q0.w, u[n][w].x, u[n][w].y);
+          mma_f16(d[n], q1.x, q1.y, q1.z, q1.w, u[n][w].z, u[n][w].w);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int row = 16 * r + 8 * g + gid;
+        const float e = base[row];
+        const int lim = edge ? len - L + 1 + (row >> lgG) : t_end;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + 2 * tig + (i & 1) + 8 * (i >> 1);
+          const float x = fmaf(d[i >> 1][2 * g + (i & 1)], f[i], e);
+          if (t < lim) sum[i] += exp2_approx(x);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    // token l's sum to lane l
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = __shfl_sync(0xffffffffu, sum[i], (lane & 7) >> 1);
+      if (i == (lane & 1) + 2 * ((lane >> 3) & 1)) v = s;
+    }
+    if (lane < 16 && t0 + lane < t_end) acc[t0 + lane] = before + v;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // --------------------------------------------------------------- eviction
@@ -414,16 +556,34 @@ __global__ void __launch_bounds__(256) gather_kernel(KvEvictArgs a, int runs) {
 
 }  // namespace evict
 
+// From this many rows on a shared cache is on the tensor cores' tcgen05 path.
+constexpr int64_t kTcRows = 128;
+
 cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st) {
   const int G = (int)(a.H / a.Hkv);
   const int64_t R = (a.len ? a.L : a.B * a.L) * G;
-  if (!a.len && R >= 128 && a.Hkv * ((a.cap + 127) / 128) <= 0x3fffffff)
+  if (!a.len && R >= kTcRows && a.Hkv * ((a.cap + 127) / 128) <= 0x3fffffff)
     return evict::launch_weights_tc(a, st);
   int lgG = 0;
   while ((1 << lgG) < G) ++lgG;
+  const int64_t caches = (a.len ? a.B : 1) * a.Hkv;
+  if (R <= 16 * evict::kMostTiles) {
+    // One CTA an SM with few tokens each, three with more: four tiles a warp.
+    const int64_t step = evict::kWarps * evict::kOwnTile;
+    int64_t s = std::max((148 + caches - 1) / caches, std::min((3 * 148 + caches - 1) / caches, a.cap / (4 * step)));
+    s = std::max((int64_t)1, std::min(s, (a.cap + step - 1) / step));
+    const int64_t part = ((a.cap + s - 1) / s + step - 1) / step * step;
+    const int splits = (int)((a.cap + part - 1) / part), tiles = (int)((R + 15) / 16);
+    auto kern = a.mode ? evict::few_rows_kernel<1> : evict::few_rows_kernel<0>;
+    const int ring = evict::kWarps * evict::kStages * (a.mode ? 2 : 1) * evict::kOwnTile * 64;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         evict::kMostTiles * nested::kFrag + ring);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)(caches * splits)), dim3(evict::kWarps * 32),
+                      tiles * nested::kFrag + ring, st, true, a, lgG, splits, (int)part);
+  }
   // The warps of a CTA share the rows of its tokens when there are more rows
   // than a warp's pass and too few tokens to give every warp its own.
-  const int64_t caches = (a.len ? a.B : 1) * a.Hkv;
   int ways = 1;
   while (ways < evict::kWarps && R > 16 * ways &&
          caches * ((a.cap + evict::kTokens - 1) / evict::kTokens) < 2 * 148 * (evict::kWarps / ways))

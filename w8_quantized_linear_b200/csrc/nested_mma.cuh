@@ -118,5 +118,37 @@ __device__ __forceinline__ void load_queries(uint32_t (&qa)[8][4], const uint16_
   }
 }
 
+// ... in shared memory (kFrag bytes) for the codes8 operand: columns 0 2 4 6 1 3
+// 5 7 of each 8, the even ones in k-step 2 w, the odd ones in 2 w + 1.
+constexpr int kFrag = 8 * 32 * 16;
+__device__ __forceinline__ void store_frag(uint4 *frag, const uint32_t (&qa)[8][4], int lane) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      const uint32_t sel = odd ? 0x7632u : 0x5410u;
+      frag[(2 * w + odd) * 32 + lane] =
+          make_uint4(prmt(qa[2 * w][0], qa[2 * w][2], sel), prmt(qa[2 * w][1], qa[2 * w][3], sel),
+                     prmt(qa[2 * w + 1][0], qa[2 * w + 1][2], sel),
+                     prmt(qa[2 * w + 1][1], qa[2 * w + 1][3], sel));
+    }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+
 }  // namespace nested
 }  // namespace bitnest

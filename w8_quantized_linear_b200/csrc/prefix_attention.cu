@@ -34,7 +34,6 @@ constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(1
 // then each warp's ring of token tiles; the ring's place holds the warps'
 // states when they join.
 constexpr int kStages = 3;
-constexpr int kFrag = 8 * 32 * 16;                          // a row tile's queries
 __host__ __device__ constexpr int stage_bytes(int mode) { return (mode ? 4 : 2) * kTile * (kD / 2); }
 struct State {
   float m[kWarps][kRows], l[kWarps][kRows];
@@ -43,22 +42,6 @@ struct State {
 constexpr int smem_bytes(int mode, int row_tiles) {
   const int ring = kWarps * kStages * stage_bytes(mode);
   return row_tiles * kFrag + (ring > (int)sizeof(State) ? ring : (int)sizeof(State));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(in ? 16 : 0)
-               : "memory");
 }
 
 // A warp's way through a cache's rows, for one lane: of each plane's tile it
@@ -387,18 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
 #pragma unroll
   for (int i = 0; i + 1 < kStages; ++i) sc[i] = load(ring + i * stage_bytes(MODE), lane);
   if (way == 0) {
-    // columns 0 2 4 6 1 3 5 7 of each 8, as codes8 gives them: the even ones are
-    // k-step 2 w's, the odd ones 2 w + 1's
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-#pragma unroll
-      for (int odd = 0; odd < 2; ++odd) {
-        const uint32_t sel = odd ? 0x7632u : 0x5410u;
-        frag[(2 * w + odd) * 32 + lane] =
-            make_uint4(prmt(qa[2 * w][0], qa[2 * w][2], sel), prmt(qa[2 * w][1], qa[2 * w][3], sel),
-                       prmt(qa[2 * w + 1][0], qa[2 * w + 1][2], sel),
-                       prmt(qa[2 * w + 1][1], qa[2 * w + 1][3], sel));
-      }
+    store_frag(frag, qa, lane);
   }
   __syncthreads();
   Part<NT> st;
@@ -638,7 +610,8 @@ cudaError_t launch_prefix_attention(const PrefixAttnArgs &a, cudaStream_t st) {
     auto kern = most <= 8 ? (a.mode ? pattn::parts_kernel<1, 1> : pattn::parts_kernel<0, 1>)
                           : (a.mode ? pattn::parts_kernel<1, 2> : pattn::parts_kernel<0, 2>);
     const int smem = pattn::smem_bytes(a.mode, p.p_ctas > 0 ? p.row_warps : 1);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         pattn::smem_bytes(a.mode, pattn::kWarps));
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)ctas), dim3(pattn::kThreads), smem, st, true, a, p, lse, o);
     if (e != cudaSuccess) return e;

@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(PrefixAttnArgs a,
   int np = pl.p_splits;
   if (pl.tc)
     np = tc_parts(pl, (h >> pl.lgG) * pl.tc_groups +
-                          ((bi << pl.lgG) + (h & (pl.G - 1))) / kTcRows);
+                          ((bi << pl.lgG) + (h & (pl.G - 1))) / pl.tc_rows);
   auto slot = [&](int s) { return (int64_t)(s < np ? s : pl.p_splits + s - np) * rows + row; };
   griddep_wait();
   griddep_launch_dependents();
@@ -529,10 +529,11 @@ bool make_plan(Plan &p, int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
   while ((1 << p.lgG) < p.G) ++p.lgG;
   const int64_t most = 0x3fffffff;
   const int64_t R = B * L * p.G;
-  p.tc = P > 0 && R >= kTcMinRows;
+  p.tc = P > 0 && R >= kTcMinRows && Hkv * ((R + 15) / 16) * ((P + 15) / 16) > kTcMinTiles;
   if (p.tc) {
-    const int64_t groups = (R + kTcRows - 1) / kTcRows, tiles = (P + kTcTokens - 1) / kTcTokens;
-    const int64_t units = Hkv * groups * tiles;
+    const int64_t tiles = (P + kTcTokens - 1) / kTcTokens, halves = (R + kTcTile - 1) / kTcTile;
+    p.tc_rows = Hkv * halves * tiles <= kSms ? kTcTile : 2 * kTcTile;
+    const int64_t groups = (R + p.tc_rows - 1) / p.tc_rows, units = Hkv * groups * tiles;
     if (units > most) return false;
     p.tc_groups = (int)groups;
     p.tc_tiles = (int)tiles;

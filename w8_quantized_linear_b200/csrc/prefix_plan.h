@@ -7,14 +7,21 @@ namespace bitnest {
 namespace pattn {
 
 constexpr int kSms = 148;
-constexpr int kTcRows = 256, kTcTokens = 128;  // of a unit on the tcgen05 path
-constexpr int64_t kTcMinRows = 64;
+constexpr int kTcTile = 128, kTcTokens = 128;  // rows of an MMA tile, tokens of a unit on the tcgen05 path
+// The tcgen05 path from 64 rows of a KV head on, but for little work: with one
+// KV head and 512 tokens the mma.sync path takes 8.6 us with 64 rows and 11.4
+// with 256 against 10.2 and 14.8; at 64 rows and 2048 tokens 10.5 against 10.6,
+// with 8 KV heads 13.1 against 13.6, and at 8192 tokens 25 against 21.
+constexpr int64_t kTcMinRows = 64, kTcMinTiles = 512;  // ... tiles of 16 rows x 16 tokens
 
 struct Plan {
   int G, lgG;           // query heads of a KV head, and their logarithm
-  // the prefix on the tensor cores' tcgen05 path: units of (256 rows of a KV
-  // head, 128 tokens), dealt to the CTAs in runs
+  // the prefix on the tensor cores' tcgen05 path: units of (tc_rows rows of a KV
+  // head, 128 tokens), dealt to the CTAs in runs; tc_rows is 256, or 128 where
+  // that still gives each CTA one unit (11.4 us instead of 14.8 at 256 rows, 512
+  // tokens and one KV head)
   bool tc;
+  int tc_rows;
   int tc_groups;        // row groups of a KV head
   int tc_tiles;         // token tiles of the prefix
   int tc_units, tc_run, tc_ctas;

@@ -3,7 +3,8 @@
 // 128 tiles, both accumulators in tensor memory, one pass with a running
 // maximum.
 //
-// A CTA takes 256 rows of one KV head (two tiles, A and B) and 128 tokens at a
+// A CTA takes 256 rows of one KV head (two tiles, A and B; only A where there
+// is little to do) and 128 tokens at a
 // time, and an equal run of such units over all KV heads and row groups.  21
 // warps:
 //   0-15   softmax of tile A (0-7) and B (8-15), 16 rows a warp, four threads a
@@ -42,7 +43,7 @@ namespace {
 using namespace nested;
 using namespace tc16;
 
-constexpr int kRowsTile = 128, kRowsCta = 256, kTokens = 128;
+constexpr int kRowsTile = kTcTile, kTokens = kTcTokens;
 constexpr int kSoftmaxWarps = 16, kOperandWarps = 4;
 constexpr int kIssueWarp = kSoftmaxWarps + kOperandWarps;
 constexpr int kThreads = (kSoftmaxWarps + kOperandWarps + 1) * 32;
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
     bool ok = true;
     while (ok && un.next(item, t0, n)) {
       const int j = item / pl.tc_groups;
-      const int first = (item % pl.tc_groups) * kRowsCta + x * kRowsTile;
-      if (first >= R) {  // no rows in tile B
+      const int first = (item % pl.tc_groups) * pl.tc_rows + x * kRowsTile;
+      if (first >= R || x * kRowsTile >= pl.tc_rows) {  // no rows in tile B
         it += n;
         continue;
       }
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         __syncwarp();
       };
       while (ok && un.next(item, t0, n)) {
-        const bool two = (item % pl.tc_groups) * kRowsCta + kRowsTile < R;
+        const bool two = pl.tc_rows > kRowsTile && (item % pl.tc_groups) * pl.tc_rows + kRowsTile < R;
         ok = wait_warp(&q_full[0], seg & 1) && (!two || wait_warp(&q_full[1], seg_b & 1)) &&
              wait_warp(&k_full[it & 1], (it >> 1) & 1);
         if (!ok) break;

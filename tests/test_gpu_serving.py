@@ -355,6 +355,49 @@ def test_prefix_attention_large_scores_and_scales(mode):
 
 
 @pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("case", [
+    (65, 4, 8, 2, 5000, 20, [i % 21 for i in range(65)]),      # 1040 rows: the last 16 alone, runs across heads
+    (96, 1, 8, 2, 9001, 3, [3] * 96),                          # 384 rows, the last 128 alone
+    (128, 2, 4, 4, 4097, 5, [5, 0, 2, 1] * 32),                # 256 rows, one token in the last tile
+    (70, 1, 8, 1, 33000, 2, [2] * 70)],                        # a long prefix, 560 rows
+    ids=lambda c: "x".join(map(str, c[:6])))
+def test_prefix_attention_of_many_rows_matches_oracle(case, mode):
+    """Runs of several units, of 256 rows, from one KV head and row group into the next."""
+    a = Attend(*case)
+    a.check(mode, bn.prefix_attention(mode, *a.d))
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("B,L,H,Hkv,P", [(40, 2, 8, 2, 1500), (300, 2, 8, 4, 3000), (3, 1, 8, 2, 700)])
+def test_prefix_attention_growing_scores_and_scales(B, L, H, Hkv, P, mode):
+    """Key and value scales that double every 100 tokens: each row's maximum and
+    the greatest value scale grow from tile to tile, so the output is rescaled
+    again and again; some tokens' values are all zero."""
+    a = Attend(B, L, H, Hkv, P, 40, [40, 17, 0][:B] + [9] * (B - 3), qscale=3.0)
+    for c, n in ((a.prefix, P), (a.own, 40)):
+        for kv in c:
+            up = np.exp2(np.minimum(np.arange(n) // 100, 9) - 6.0)[:, None]
+            kv[2][...] = (kv[2].astype(np.float64) * up).astype(np.float16)
+        c[1][2].reshape(-1)[::13] = 0.0
+    a.upload()
+    a.check(mode, bn.prefix_attention(mode, *a.d))
+
+
+@pytest.mark.parametrize("B,L,H,Hkv,P", [(40, 2, 8, 2, 1500), (300, 2, 8, 4, 3000), (3, 1, 8, 2, 700)])
+def test_prefix_attention_shows_nan(B, L, H, Hkv, P):
+    """A query with a NaN gives NaN in its own row and nowhere else."""
+    a = Attend(B, L, H, Hkv, P, 40, [40, 17, 0][:B] + [9] * (B - 3))
+    want = bn.prefix_attention(1, *a.d)
+    q = a.d[0].clone()
+    q[1, 0, 3, 77] = float("nan")
+    got = bn.prefix_attention(1, q, *a.d[1:])
+    row = torch.zeros(B, L, H, dtype=torch.bool, device="cuda")
+    row[1, 0, 3] = True
+    assert torch.all(got[0][row].isnan()) and torch.all(got[1][row].isnan())
+    assert torch.equal(got[0][~row], want[0][~row]) and torch.equal(got[1][~row], want[1][~row])
+
+
+@pytest.mark.parametrize("mode", [0, 1])
 def test_prefix_attention_hidden_rows_may_hold_anything(mode):
     """Rows behind a sequence's length with NaN and infinite scales, scratch full
     of NaN: the same bits; a sequence of negative length keeps its outputs."""

@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
     row_base = b * a.cap * Hkv + j;
     const int len = min(__ldg(a.len + b), (int)a.cap);
     t_begin = split * pl.o_len;
-    if (t_begin >= len) {  // also a sequence that is not taking part: the join reads no such part
+    if (t_begin >= len) {  // no tokens: no weight (nothing reads the parts of len < 0)
+      const int r = row0 + (int)threadIdx.x;
+      if (threadIdx.x < kRows && r < R)
+        part_lse[(int64_t)(pl.p_splits + split) * rows_out + query_row(bi0, r, lgG, H, j)] = -INFINITY;
       if (pl.tc) griddep_wait();
       return;
     }
@@ -456,13 +459,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(PrefixAttnArgs a,
   auto slot = [&](int s) { return (int64_t)(s < np ? s : pl.p_splits + s - np) * rows + row; };
   griddep_wait();
   griddep_launch_dependents();
-  const int len = min(a.len[bi / L], (int)a.cap);
-  const int own = len > 0 ? (len - 1) / pl.o_len + 1 : 0;
-  const int parts = np + own, mine = parts > way ? (parts - way - 1) / ways + 1 : 0;
-  float M = -INFINITY;
+  const int len = a.len[bi / L];
+  const int parts = np + pl.o_splits, mine = parts > way ? (parts - way - 1) / ways + 1 : 0;
+  // few parts: their outputs are read beside their weights, needed or not
+  constexpr int kFew = 4;
+  const bool few = mine <= kFew;
+  float4 early[kFew];
+  if (few) {
+#pragma unroll
+    for (int s = 0; s < kFew; ++s)
+      if (s < mine) early[s] = reinterpret_cast<const float4 *>(part_o + slot(way + s * ways) * kD)[lane];
+  }
+  float M = -INFINITY, first = -INFINITY;
   bool nan = false;  // fmaxf passes over NaN, which the output must show
   for (int s = lane; s < mine; s += 32) {
     const float v = part_lse[slot(way + s * ways)];
+    if (s == lane) first = v;
     M = fmaxf(M, v);
     nan |= v != v;
   }
@@ -470,20 +482,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(PrefixAttnArgs a,
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   if (__any_sync(0xffffffffu, nan)) M = NAN;
   float den = 0.0f, o[4] = {};
+  auto add = [&](float w, const float4 &v) {
+    den += w;
+    o[0] += w * v.x;
+    o[1] += w * v.y;
+    o[2] += w * v.z;
+    o[3] += w * v.w;
+  };
   if (M != -INFINITY)
     for (int s0 = 0; s0 < mine; s0 += 32) {
-      const int n = min(32, mine - s0);
-      const float f = lane < n ? exp2f(part_lse[slot(way + (s0 + lane) * ways)] - M) : 0.0f;
-#pragma unroll 8
-      for (int s = 0; s < n; ++s) {
-        const float w = __shfl_sync(0xffffffffu, f, s);
-        float4 v = reinterpret_cast<const float4 *>(part_o + slot(way + (s0 + s) * ways) * kD)[lane];
-        if (w == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // a part without weight writes none
-        den += w;
-        o[0] += w * v.x;
-        o[1] += w * v.y;
-        o[2] += w * v.z;
-        o[3] += w * v.w;
+      const int at = s0 + lane;
+      const float ls = s0 == 0 ? first : at < mine ? part_lse[slot(way + at * ways)] : -INFINITY;
+      const float f = at < mine ? exp2f(ls - M) : 0.0f;
+      if (few) {
+#pragma unroll
+        for (int s = 0; s < kFew; ++s) {
+          const float w = __shfl_sync(0xffffffffu, f, s);
+          if (w != 0.0f) add(w, early[s]);  // a part without weight writes no output
+        }
+        break;
+      }
+      // the parts with weight, four at a time
+      uint32_t left = __ballot_sync(0xffffffffu, f != 0.0f);
+      while (left) {
+        float w[4];
+        float4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int s = left ? __ffs(left) - 1 : 0;
+          w[i] = __shfl_sync(0xffffffffu, f, s);
+          if (!left) w[i] = 0.0f;
+          if (left) v[i] = reinterpret_cast<const float4 *>(part_o + slot(way + (s0 + s) * ways) * kD)[lane];
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (w[i] != 0.0f) add(w[i], v[i]);
       }
     }
   if (ways > 1) {  // the same for the whole grid

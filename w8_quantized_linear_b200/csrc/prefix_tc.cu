@@ -5,7 +5,7 @@
 //
 // A CTA takes 256 rows of one KV head (two tiles, A and B; only A where there
 // is little to do) and 128 tokens at a
-// time, and an equal run of such units over all KV heads and row groups.  21
+// time, and an equal run of such units over all KV heads and row groups.  25
 // warps:
 //   0-15   softmax of tile A (0-7) and B (8-15), 16 rows a warp, four threads a
 //          row (so that a token's scales serve two rows of a thread, and a
@@ -13,9 +13,9 @@
 //          times the tokens' K scales, the row's running maximum,
 //          p = 2^(s - shift), times the V scales, rounded to fp16 and written
 //          back over the scores as the second product's A operand;
-//   16-19  the cache's codes as fp16 operands: plane words -> shared memory
+//   16-23  the cache's codes as fp16 operands: plane words -> shared memory
 //          (128-byte swizzle), two stages of K and of V; the tokens' scales;
-//   20     issues the MMAs.
+//   24     issues the MMAs.
 // The tensor cores work on tile B while A is in its softmax and back.
 //
 // The codes are exact in fp16, so a score is off by fp32 sums only.  The
@@ -44,10 +44,12 @@ using namespace nested;
 using namespace tc16;
 
 constexpr int kRowsTile = kTcTile, kTokens = kTcTokens;
-constexpr int kSoftmaxWarps = 16, kOperandWarps = 4;
+constexpr int kSoftmaxWarps = 16, kOperandWarps = 8;
+constexpr int kWords = 16 / kOperandWarps;  // rows of a tile for an operand thread
 constexpr int kIssueWarp = kSoftmaxWarps + kOperandWarps;
 constexpr int kThreads = (kSoftmaxWarps + kOperandWarps + 1) * 32;
 constexpr int kStages = 2, kSlots = 4;
+constexpr int kHalf = kTokens / 2;
 constexpr int kOperand = kTokens * kD * 2;  // bytes of a K, V or Q tile
 constexpr float kScale = 0.088388347648318440550f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kSlack = 8.0f;
@@ -63,7 +65,7 @@ constexpr int kScaleRow = 36, kScaleSet = 4 * kScaleRow;
 constexpr int kOffScale = kOffV + kStages * kOperand;        // [slot][k, v][kScaleSet] floats
 constexpr int kOffExp = kOffScale + kSlots * 2 * kScaleSet * 4;  // [slot][4] ints
 constexpr int kOffBar = kOffExp + kSlots * 4 * 4;
-constexpr int kBars = 4 * kStages + kSlots + 2 * 4 + 1;
+constexpr int kBars = 4 * kStages + kSlots + 2 + 4 + 4 + 2 + 1;
 constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 
 constexpr int kColO = 0, kColS = 256;  // tensor memory columns (tile B: + 128)
@@ -86,10 +88,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// One thread's share of a tile's plane rows: for q = 0 .. 3, 16 bytes (piece
-// tid / 8 % 4) of the row of token 32 q + 8 (tid / 32) + tid % 8.
+// One operand thread's share of a tile's plane rows: for q < kWords, 16 bytes
+// (piece tid / 8 % 4) of the row of token 8 kOperandWarps q + 8 (tid / 32) + tid % 8.
+constexpr int kRowStep = 8 * kOperandWarps;
 struct Words {
-  uint4 hi[4], lo[4];
+  uint4 hi[kWords], lo[kWords];
 };
 struct Rows {  // where a thread's rows of a tile are
   int64_t t, off;
@@ -103,8 +106,8 @@ __device__ __forceinline__ void load_words(Words &w, int q, const uint8_t *__res
                                            const uint8_t *__restrict__ lo, const Rows &r,
                                            int64_t P, int64_t Hkv) {
   w.hi[q] = w.lo[q] = make_uint4(0, 0, 0, 0);
-  if (r.t + 32 * q < P) {
-    const int64_t off = r.off + q * 32 * Hkv * (kD / 2);
+  if (r.t + kRowStep * q < P) {
+    const int64_t off = r.off + q * kRowStep * Hkv * (kD / 2);
     w.hi[q] = __ldg(reinterpret_cast<const uint4 *>(hi + off));
     if (MODE) w.lo[q] = __ldg(reinterpret_cast<const uint4 *>(lo + off));
   }
@@ -115,7 +118,7 @@ __device__ __forceinline__ void load_words(Words &w, int q, const uint8_t *__res
 template <int MODE>
 __device__ __forceinline__ void store_words(uint8_t *dst, const Words &w, int q, int tid) {
   const int piece = (tid >> 3) & 3, t = 8 * (tid >> 5) + (tid & 7);
-  uint8_t *row = dst + (piece >> 1) * (kOperand / 2) + (t + 32 * q) * 128;
+  uint8_t *row = dst + (piece >> 1) * (kOperand / 2) + (t + kRowStep * q) * 128;
   const uint32_t h[4] = {w.hi[q].x, w.hi[q].y, w.hi[q].z, w.hi[q].w};
   const uint32_t l[4] = {w.lo[q].x, w.lo[q].y, w.lo[q].z, w.lo[q].w};
 #pragma unroll
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
   uint64_t *k_full = bars, *k_free = k_full + kStages, *v_full = k_free + kStages,
            *v_free = v_full + kStages, *sc_full = v_free + kStages, *q_full = sc_full + kSlots,
-           *s_full = q_full + 2, *p_full = s_full + 2, *o_done = p_full + 2, *last_done = o_done + 2;
+           *s_full = q_full + 2, *p_full = s_full + 4, *o_done = p_full + 4, *last_done = o_done + 2;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = (int)a.Hkv, lgG = pl.lgG;
@@ -157,17 +160,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   if (threadIdx.x == 0) {
     mbar_init(last_done, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], 4);
+      mbar_init(&k_full[s], kOperandWarps);
       mbar_init(&k_free[s], 1);
-      mbar_init(&v_full[s], 4);
+      mbar_init(&v_full[s], kOperandWarps);
       mbar_init(&v_free[s], 1);
     }
     for (int s = 0; s < kSlots; ++s) mbar_init(&sc_full[s], 4);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], kSoftmaxWarps / 2);
+      mbar_init(&o_done[x], 1);
+    }
+    for (int x = 0; x < 4; ++x) {  // [row tile][half of the token tile]
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], kSoftmaxWarps / 2);
-      mbar_init(&o_done[x], 1);
     }
     fence_barrier_init();
   }
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
     const int x = warp >> 3, first_row = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
     const uint32_t ts = tmem + ((uint32_t)first_row << 16) + kColS + 128 * x,
                    to = tmem + ((uint32_t)first_row << 16) + kColO + 128 * x;
-    int it = 0, sx = 0;  // tiles of the CTA, tiles of this row tile
+    int it = 0, su = 0;  // token tiles of the CTA, half tiles of this row tile
     bool ok = true;
     while (ok && un.next(item, t0, n)) {
       const int j = item / pl.tc_groups;
@@ -225,48 +230,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
       int e = kMinExp;
 #pragma unroll
       for (int r = 0; r < 2; ++r) m[r] = shift[r] = sum[r][0] = sum[r][1] = 0.0f;
-      for (int i = 0; i < n; ++i, ++it, ++sx) {
-        const int slot = it & (kSlots - 1);
-        const float *ks = scales + slot * 2 * kScaleSet + (lane & 3) * kScaleRow, *vs = ks + kScaleSet;
+      for (int i = 0; i < 2 * n; ++i, ++su) {
+        const int half = i & 1, slot = (it + (i >> 1)) & (kSlots - 1);
+        const uint32_t th = ts + kHalf * half;
+        const float *ks = scales + slot * 2 * kScaleSet + (lane & 3) * kScaleRow + 16 * half, *vs = ks + kScaleSet;
         // the scores first: a tile that skipped row groups is then no further
         // than one phase from the scales' barrier, which has no count of its own
-        ok = wait_warp(&s_full[x], sx & 1) && wait_warp(&sc_full[slot], (it / kSlots) & 1);
+        ok = wait_warp(&s_full[2 * x + half], (su >> 1) & 1) &&
+             wait_warp(&sc_full[slot], ((it + (i >> 1)) / kSlots) & 1);
         if (!ok) break;
         tc_fence_after();
-        const int left = (int)a.P - (t0 + i) * kTokens;
-        if (left < kTokens) {  // the prefix ends inside the tile: its scales there are 1 and 0
-          for (int c = left >> 3; c < kTokens / 8; ++c) {
-            float o[4];
-            ld_16x8(ts + 8 * c, o);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = 8 * c + 2 * (lane & 3) + (k & 1) < left ? o[k] : -INFINITY;
-            st_16x8(ts + 8 * c, o);
-          }
-          tmem_st_wait();
-        }
-        // first pass: the maximum; the second reads the scores once more, so
-        // that 64 tokens are all that registers hold
         float t[32], tm[2] = {-INFINITY, -INFINITY};
+        ld_16x64(th, t);
+        ld_wait32(t);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          ld_16x64(ts + 64 * g, t);
-          ld_wait32(t);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * g + 4 * k);
-            float *p = t + 8 * k;
-            f32x2_mul(p[0], p[1], p[0], p[1], k4.x, k4.y);
-            f32x2_mul(p[2], p[3], p[2], p[3], k4.x, k4.y);
-            f32x2_mul(p[4], p[5], p[4], p[5], k4.z, k4.w);
-            f32x2_mul(p[6], p[7], p[6], p[7], k4.z, k4.w);
-            tm[0] = max3(tm[0], p[0], p[1]);
-            tm[1] = max3(tm[1], p[2], p[3]);
-            tm[0] = max3(tm[0], p[4], p[5]);
-            tm[1] = max3(tm[1], p[6], p[7]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float4 k4 = *reinterpret_cast<const float4 *>(ks + 4 * k);
+          float *p = t + 8 * k;
+          f32x2_mul(p[0], p[1], p[0], p[1], k4.x, k4.y);
+          f32x2_mul(p[2], p[3], p[2], p[3], k4.x, k4.y);
+          f32x2_mul(p[4], p[5], p[4], p[5], k4.z, k4.w);
+          f32x2_mul(p[6], p[7], p[6], p[7], k4.z, k4.w);
         }
-        ld_16x64(ts, t);
+        const int left = (int)a.P - (t0 + (i >> 1)) * kTokens - kHalf * half;
+        if (left < kHalf) {  // the prefix ends inside the half tile, or before it
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            t[k] = 8 * (k >> 2) + 2 * (lane & 3) + (k & 1) < left ? t[k] : -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          tm[0] = max3(tm[0], t[k], t[k + 1]);
+          tm[1] = max3(tm[1], t[k + 2], t[k + 3]);
+        }
         const int4 e4 = *reinterpret_cast<const int4 *>(exps + 4 * slot);
         const int e_new = max(max(e, max(e4.x, e4.y)), max(e4.z, e4.w));
         bool grown = e_new > e;
@@ -295,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
             sum[r][0] *= f[r];
             sum[r][1] *= f[r];
           }
-          ok = wait_warp(&o_done[x], (sx - 1) & 1);  // the output so far is complete
+          ok = wait_warp(&o_done[x], (su - 1) & 1);  // the output so far is complete
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -307,37 +303,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
             st_16x8(to + 8 * c, o);
           }
         }
+        uint32_t pk[16];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          ld_wait32(t);
-          uint32_t pk[16];
+        for (int k = 0; k < 4; ++k) {
+          float *p = t + 8 * k;
+          const float4 v4 = *reinterpret_cast<const float4 *>(vs + 4 * k);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float *p = t + 8 * k;
-            const float4 k4 = *reinterpret_cast<const float4 *>(ks + 16 * g + 4 * k);
-            const float4 v4 = *reinterpret_cast<const float4 *>(vs + 16 * g + 4 * k);
-#pragma unroll
-            for (int q = 0; q < 8; q += 2) {  // row lane / 4 + 8 (q / 2 % 2), two tokens
-              const int r = (q >> 1) & 1;
-              f32x2_fma(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? k4.x : k4.z, q < 4 ? k4.y : k4.w,
-                        -shift[r], -shift[r]);
-              p[q] = exp2_approx(p[q]);
-              p[q + 1] = exp2_approx(p[q + 1]);
-              f32x2_add(sum[r][0], sum[r][1], sum[r][0], sum[r][1], p[q], p[q + 1]);
-              f32x2_mul(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? v4.x : v4.z, q < 4 ? v4.y : v4.w);
-              pk[4 * k + q / 2] = pack_half2(p[q], p[q + 1]);
-            }
+          for (int q = 0; q < 8; q += 2) {  // row lane / 4 + 8 (q / 2 % 2), two tokens
+            const int r = (q >> 1) & 1;
+            f32x2_sub(p[q], p[q + 1], p[q], p[q + 1], shift[r], shift[r]);
+            p[q] = exp2_approx(p[q]);
+            p[q + 1] = exp2_approx(p[q + 1]);
+            f32x2_add(sum[r][0], sum[r][1], sum[r][0], sum[r][1], p[q], p[q + 1]);
+            f32x2_mul(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? v4.x : v4.z, q < 4 ? v4.y : v4.w);
+            pk[4 * k + q / 2] = pack_half2(p[q], p[q + 1]);
           }
-          if (g == 0) ld_16x64(ts + 64, t);  // behind the columns that the weights overwrite
-          st_16x32(ts + 32 * g, pk);
         }
+        st_16x32(th, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
       }
+      it += n;
       if (!ok) break;
-      ok = wait_warp(&o_done[x], (sx - 1) & 1);
+      // the last two outputs in turn (the scores of a half tell of all but those)
+      ok = wait_warp(&o_done[x], su & 1) && wait_warp(&o_done[x], (su - 1) & 1);
       if (!ok) break;
       tc_fence_after();
       const int64_t part = (int64_t)((int)blockIdx.x - tc_first_cta(pl, item)) * rows_out;
@@ -377,98 +368,113 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   } else if (warp < kIssueWarp) {
     const int tid = threadIdx.x - 32 * kSoftmaxWarps, w = warp - kSoftmaxWarps;
     const KvPlanes &c = a.prefix;
-    int it = 0;
-    bool ok = true, more = un.next(item, t0, n);
-    // K words and scales are loaded while the V before is written, V words
-    // while K is: 64 words at a time in registers
-    Words kv;
+    // The CTA's token tiles one after the other, across row groups: K of the
+    // next tile, then V of this one.  Each has words of its own in registers,
+    // loaded as soon as the ones before are written: a load is in flight while
+    // the other operand is written.
+    const int tiles = un.end - un.u;
+    struct Cursor {  // the tile to load next
+      Units un;
+      int item, t, n;
+      __device__ __forceinline__ void step() {
+        ++t;
+        if (--n == 0) un.next(item, t, n);
+      }
+    } ck, cv;
+    ck.un = un;
+    ck.un.next(ck.item, ck.t, ck.n);
+    cv = ck;
+    Words kw, vw;
     uint16_t sk = 0, sv = 0;
-    auto load_scales = [&](int64_t tok, int j) {
+    auto load_k = [&]() {
+      const int j = ck.item / pl.tc_groups;
+      const Rows r = rows_of((int64_t)ck.t * kTokens, Hkv, j, tid);
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) load_words<MODE>(kw, q, c.k_hi, c.k_lo, r, a.P, Hkv);
+      const int64_t tok = (int64_t)ck.t * kTokens + tid;
       sk = sv = 0;
-      if (tok + tid < a.P) {
-        sk = __ldg(c.k_scale + (tok + tid) * Hkv + j);
-        sv = __ldg(c.v_scale + (tok + tid) * Hkv + j);
+      if (w < 4 && tok < a.P) {
+        sk = __ldg(c.k_scale + tok * Hkv + j);
+        sv = __ldg(c.v_scale + tok * Hkv + j);
       }
+      ck.step();
     };
-    if (more) {
-      const int j = item / pl.tc_groups;
-      const Rows r = rows_of((int64_t)t0 * kTokens, Hkv, j, tid);
+    auto load_v = [&]() {
+      const Rows r = rows_of((int64_t)cv.t * kTokens, Hkv, cv.item / pl.tc_groups, tid);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) load_words<MODE>(kv, q, c.k_hi, c.k_lo, r, a.P, Hkv);
-      load_scales((int64_t)t0 * kTokens, j);
-    }
-    while (ok && more) {
-      const int64_t tok = (int64_t)t0 * kTokens;
+      for (int q = 0; q < kWords; ++q) load_words<MODE>(vw, q, c.v_hi, c.v_lo, r, a.P, Hkv);
+      cv.step();
+    };
+    auto store_k = [&](int it) {
       const int s = it & (kStages - 1), slot = it & (kSlots - 1);
-      const uint32_t free_parity = ((it / kStages) & 1) ^ 1;
-      const Rows rv = rows_of(tok, Hkv, item / pl.tc_groups, tid);
-      ok = wait_warp(&k_free[s], free_parity);
-      if (!ok) break;
-      const bool in = tok + tid < a.P;  // behind the prefix: scales 1 and 0
-      const float fk = in ? half_bits(sk) * (MODE ? 0.0625f * kScale : kScale) : 1.0f;
-      const float fv = half_bits(sv) * (MODE ? 0.0625f : 1.0f);
-      const int sc = slot * 2 * kScaleSet + ((tid >> 1) & 3) * kScaleRow + 2 * (tid >> 3) + (tid & 1);
-      scales[sc] = fk;
-      scales[sc + kScaleSet] = fv;
-      int e = fv > 0.0f ? (int)((__float_as_uint(fv) >> 23) & 0xFFu) - 126 : kMinExp;
-      e = __reduce_max_sync(0xffffffffu, min(e, 40));
-      if (lane == 0) exps[4 * slot + w] = e;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        store_words<MODE>(sm + kOffK + s * kOperand, kv, q, tid);
-        load_words<MODE>(kv, q, c.v_hi, c.v_lo, rv, a.P, Hkv);
+      if (!wait_warp(&k_free[s], ((it / kStages) & 1) ^ 1)) return false;
+      if (w < 4) {  // a token's scales for each of 128 threads
+        const float fk = half_bits(sk) * (MODE ? 0.0625f * kScale : kScale);
+        const float fv = half_bits(sv) * (MODE ? 0.0625f : 1.0f);
+        const int sc = slot * 2 * kScaleSet + ((tid >> 1) & 3) * kScaleRow + 2 * (tid >> 3) + (tid & 1);
+        scales[sc] = fk;
+        scales[sc + kScaleSet] = fv;
+        int e = fv > 0.0f ? (int)((__float_as_uint(fv) >> 23) & 0xFFu) - 126 : kMinExp;
+        e = __reduce_max_sync(0xffffffffu, min(e, 40));
+        if (lane == 0) exps[4 * slot + w] = e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[slot]);
       }
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) store_words<MODE>(sm + kOffK + s * kOperand, kw, q, tid);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sc_full[slot]);
-        mbar_arrive(&k_full[s]);
-      }
-      // the next tile
-      ++t0;
-      if (--n == 0) more = un.next(item, t0, n);
-      const int j = item / pl.tc_groups;
-      const Rows rk = rows_of((int64_t)t0 * kTokens, Hkv, j, tid);
-      ok = wait_warp(&v_free[s], free_parity);
+      if (lane == 0) mbar_arrive(&k_full[s]);
+      if (it + 1 < tiles) load_k();
+      return true;
+    };
+    bool ok = true;
+    if (tiles > 0) {
+      load_k();
+      load_v();
+      ok = store_k(0) && (tiles == 1 || store_k(1));
+    }
+    for (int it = 0; ok && it < tiles; ++it) {
+      const int s = it & (kStages - 1);
+      ok = wait_warp(&v_free[s], ((it / kStages) & 1) ^ 1);
       if (!ok) break;
-      if (more) load_scales((int64_t)t0 * kTokens, j);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        store_words<MODE>(sm + kOffV + s * kOperand, kv, q, tid);
-        if (more) load_words<MODE>(kv, q, c.k_hi, c.k_lo, rk, a.P, Hkv);
-      }
+      for (int q = 0; q < kWords; ++q) store_words<MODE>(sm + kOffV + s * kOperand, vw, q, tid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[s]);
-      ++it;
+      if (it + 1 < tiles) load_v();
+      if (it + 2 < tiles) ok = store_k(it + 2);
     }
   } else {
     {
       const uint64_t qd = umma_desc_sw128(sm + kOffQ), kd = umma_desc_sw128(sm + kOffK),
                      vd = desc_mn_sw128(sm + kOffV);
       constexpr uint64_t kOp = kOperand >> 4;  // descriptor address unit: 16 bytes
-      int it = 0, seg = 0, seg_b = 0, sx[2] = {0, 0};
+      int it = 0, seg = 0, seg_b = 0, su[2] = {0, 0};
       bool ok = true, issued = false;
       // The whole warp runs along and one elected thread issues.
-      auto scores = [&](int x, int s) {  // S_x = Q_x K^T: 8 k-steps of 16 columns
+      // S_x = Q_x K^T for a half of the token tile in stage s: 8 k-steps of 16 columns
+      auto scores = [&](int x, int s, int half) {
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint64_t step = (k >> 2) * (kOp / 2) + 2 * (k & 3);
-            mma_ss(tmem + kColS + 128 * x, qd + x * kOp + step, kd + s * kOp + step, idesc(false),
-                   k > 0);
+            mma_ss(tmem + kColS + 128 * x + kHalf * half, qd + x * kOp + step,
+                   kd + s * kOp + half * (kHalf * 128 >> 4) + step, idesc(false, kHalf), k > 0);
           }
-          umma_commit(&s_full[x]);
+          umma_commit(&s_full[2 * x + half]);
         }
         __syncwarp();
         issued = true;
       };
-      auto output = [&](int x, int s, bool add) {  // O_x += P_x V: 8 k-steps of 16 tokens
+      // O_x += P_x V for a half: 4 k-steps of 16 tokens
+      auto output = [&](int x, int s, int half, bool add) {
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * k,
-                   vd + s * kOp + (2048 >> 4) * k, idesc(true), add || k > 0);
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + kHalf * half + 8 * k,
+                   vd + s * kOp + (2048 >> 4) * (4 * half + k), idesc(true, kD), add || k > 0);
           umma_commit(&o_done[x]);
         }
         __syncwarp();
@@ -485,36 +491,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         ++seg;
         seg_b += two;
         tc_fence_after();
-        scores(0, it & 1);
-        if (two) scores(1, it & 1);
+        for (int half = 0; half < 2; ++half) {
+          scores(0, it & 1, half);
+          if (two) scores(1, it & 1, half);
+        }
         commit(&k_free[it & 1]);
+        // Scores are a token tile ahead: each half's are computed into the place of
+        // the weights that its output has just used up.
         for (int i = 0; i < n; ++i, ++it) {
           const int s = it & 1, s2 = (it + 1) & 1;
-          const uint32_t ph = (it >> 1) & 1, ph2 = ((it + 1) >> 1) & 1;
           const bool last = i + 1 == n;
-          ok = wait_warp(&v_full[s], ph) && wait_warp(&p_full[0], sx[0] & 1);
+          ok = wait_warp(&v_full[s], (it >> 1) & 1) && (last || wait_warp(&k_full[s2], ((it + 1) >> 1) & 1));
           if (!ok) break;
-          tc_fence_after();
-          output(0, s, i > 0);
-          ++sx[0];
-          if (!last) {
-            ok = wait_warp(&k_full[s2], ph2);
-            if (!ok) break;
-            tc_fence_after();
-            scores(0, s2);
+          for (int half = 0; ok && half < 2; ++half) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x == 1 && !two) break;
+              ok = ok && wait_warp(&p_full[2 * x + half], (su[x] >> 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              output(x, s, half, i > 0 || half > 0);
+              ++su[x];
+              if (!last) scores(x, s2, half);
+            }
           }
-          if (two) {
-            ok = wait_warp(&p_full[1], sx[1] & 1);
-            if (!ok) break;
-            tc_fence_after();
-            output(1, s, i > 0);
-            ++sx[1];
-          }
+          if (!ok) break;
           commit(&v_free[s]);
-          if (!last) {
-            if (two) scores(1, s2);
-            commit(&k_free[s2]);
-          }
+          if (!last) commit(&k_free[s2]);
         }
       }
       // what was issued must end before tensor memory and the barriers go

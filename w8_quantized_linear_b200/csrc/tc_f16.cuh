@@ -9,9 +9,9 @@ namespace bitnest {
 namespace tc16 {
 
 // kind::f16 with fp32 accumulation: A fp16 (K-major), B fp16 (K-major, or
-// MN-major when bn), 128 x 128
-constexpr uint32_t idesc(bool bn) {
-  return (1u << 4) | (bn ? 1u << 16 : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+// MN-major when bn), 128 x N
+constexpr uint32_t idesc(bool bn, int N = 128) {
+  return (1u << 4) | (bn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] B[smem]

@@ -647,6 +647,63 @@ def test_captured_and_on_another_stream():
                    for g, t in zip(flat(r, st), w))
 
 
+def test_captured_attention_and_weights_of_many_rows():
+    """The tcgen05 kernels, own tokens beside them, captured once and replayed on
+    new inputs, and on a side stream: the same bits as on the default stream."""
+    cases = [Attend(70, 2, 8, 2, 6000, 50, [(7 * i + s) % 51 for i in range(70)], seed=s) for s in range(3)]
+
+    def step(q, prefix, own, lens, acc):
+        out, lse = bn.prefix_attention(1, q, prefix, own, lens)
+        bn.kv_weights(1, q, lse, prefix[0], acc)
+        return out, lse
+
+    want = []
+    for a in cases:
+        acc = torch.zeros(2, 6000, device="cuda")
+        want.append((*step(*a.d, acc), acc))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for a, w in zip(cases, want):
+            acc = torch.zeros(2, 6000, device="cuda")
+            got = (*step(*a.d, acc), acc)
+            side.synchronize()
+            assert all(torch.equal(g, t) for g, t in zip(got, w))
+    flat = lambda d: [d[0], *(t for c in d[1:3] for pl in c for t in pl), d[3]]  # noqa: E731
+    held = Attend(70, 2, 8, 2, 6000, 50, [0] * 70, seed=9)
+    acc = torch.zeros(2, 6000, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        acc.zero_()
+        r = step(*held.d, acc)
+    for a, w in zip(cases, want):
+        for old, new in zip(flat(held.d), flat(a.d)):
+            old.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, t) for g, t in zip((*r, acc), w))
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+def test_weights_of_many_own_rows(mode):
+    """More than 128 rows of one sequence's KV head."""
+    a = Attend(3, 40, 8, 2, 0, 300, [300, 41, 7])
+    lse = (np.random.default_rng(1).standard_normal((3, 40, 8)) + 6.0).astype(np.float32)
+    acc = torch.zeros(3, 2, 300, device="cuda")
+    got = host(bn.kv_weights(mode, a.d[0], dev(lse), a.d[2][0], acc, a.d[3]))
+    want = ref.weights(mode, a.q, lse, a.own[0], np.zeros((3, 2, 300)), a.lens)
+    rel = a.bounds(mode, lse.astype(np.float64), 0.0, 0.0)[1].max() + (160 + 2) * U
+    assert np.all(np.abs(got - want) <= rel * want)
+
+
+def test_attention_of_nothing():
+    """A prefix of no tokens and an empty cache: zeros and -inf."""
+    q = torch.randn(2, 1, 4, 128, device="cuda").half()
+    own = bn.nested_cache(0, 2, 2)
+    out, lse = bn.prefix_attention(1, q, bn.nested_cache(0, 2), own, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert torch.all(out == 0) and torch.all(lse == -torch.inf)
+
+
 def test_two_calls_at_once():
     """Two attentions at the same time on two streams, each with scratch of its own."""
     cases = [Attend(8, 4, 16, 2, 2000, 100, [i * 12 for i in range(8)], seed=s) for s in range(2)]

@@ -103,7 +103,7 @@ struct Loader {
 // shift), shift = m + e - kHead with m a maximum at most kSlack behind and 2^e
 // above every V scale so far: the output is rescaled only when one of them has
 // grown, and p v_scale < 2^15 enters the product as one fp16 term (11 bits:
-// 2^-12 of each weight at most, as the fp16 output's own rounding is).
+// 2^-11 of each weight at most, as the fp16 output's own rounding is).
 // e with vmax < 2^e, at most 100 (an infinite scale)
 __device__ __forceinline__ int e_tile_of(float vmax) {
   return vmax > 0.0f ? min(100, (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126) : kMinExp;
@@ -576,7 +576,8 @@ bool make_plan(Plan &p, int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
     // SMs for the own tokens
     p.tc_run = (int)((units + kSms - 1) / kSms);
     p.tc_ctas = (int)((units + p.tc_run - 1) / p.tc_run);
-    for (int item = 0; item < Hkv * groups; ++item) p.p_splits = max(p.p_splits, tc_parts(p, item));
+    // the most CTAs whose runs meet one item's units
+    p.p_splits = (int)min((int64_t)p.tc_ctas, (tiles + p.tc_run - 2) / p.tc_run + 1);
   } else if (P > 0) {
     const int64_t row_tiles = (R + kRows - 1) / kRows;
     p.row_warps = row_tiles >= 8 ? 8 : row_tiles >= 4 ? 4 : row_tiles >= 2 ? 2 : 1;

@@ -512,7 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
               tc_fence_after();
               output(x, s, half, i > 0 || half > 0);
               ++su[x];
-              if (!last) scores(x, s2, half);
+            }
+            // products into different columns are not bound to run in order: the scores
+            // wait for the output that still reads the weights in their place
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (last || (x == 1 && !two)) break;
+              ok = ok && wait_warp(&o_done[x], (su[x] - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(x, s2, half);
             }
           }
           if (!ok) break;

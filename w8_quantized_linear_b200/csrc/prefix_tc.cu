@@ -16,7 +16,15 @@
 //   16-23  the cache's codes as fp16 operands: plane words -> shared memory
 //          (128-byte swizzle), two stages of K and of V; the tokens' scales;
 //   24     issues the MMAs.
-// The tensor cores work on tile B while A is in its softmax and back.
+// The tensor cores work on tile B while A is in its softmax and back; scores are
+// computed a token tile ahead, in halves of 64 tokens, each into the place of the
+// weights that the output before has used up.
+//
+// Measured: 128 x 4 queries of 32 heads over 16384 target tokens (8192 units, 56 a
+// CTA) 205 us, 667 TFLOP/s, about 6000 cycles a unit: its MMAs need 2048, its
+// exponentials 2048 (16 a cycle and SM); the SM's load/store pipe, which tensor
+// memory reads and writes, scales and operands share, is busy 80 % of the time.
+// Scores held in registers for both passes by fewer warps were slower.
 //
 // The codes are exact in fp16, so a score is off by fp32 sums only.  The
 // output is rescaled only when a row's maximum has grown by 2^8 or the largest

@@ -17,7 +17,8 @@
 //   21     brings the row tiles (TMA) and their lse.
 //
 // Bound: the exponentials.  16 a cycle and SM make 1024 cycles a product of
-// 128 x 128, its MMAs 512.
+// 128 x 128, its MMAs 512.  64 x 4 queries of 32 heads over 16384 tokens: 50 us,
+// 689 TFLOP/s, of which the exponentials are 31 at least.
 #include <cudaTypedefs.h>
 #include <math.h>
 

@@ -16,9 +16,11 @@
 //   20     issues the MMAs;
 //   21     brings the row tiles (TMA) and their lse.
 //
-// Bound: the exponentials.  16 a cycle and SM make 1024 cycles a product of
-// 128 x 128, its MMAs 512.  64 x 4 queries of 32 heads over 16384 tokens: 50 us,
-// 689 TFLOP/s, of which the exponentials are 31 at least.
+// The exponentials, 16 a cycle and SM, make 1024 cycles a product of 128 x 128, its
+// MMAs 512.  64 x 4 queries of 32 heads over 16384 tokens: 50 us, 689 TFLOP/s, of
+// which the exponentials are 31 at least (their unit is busy 63 % of the time); a
+// quarter of them as polynomials on the FMA pipe instead takes 52: what is left is
+// the reading of tensor memory and the slots' hand-over.
 #include <cudaTypedefs.h>
 #include <math.h>
 

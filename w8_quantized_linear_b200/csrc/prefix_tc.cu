@@ -73,7 +73,7 @@ constexpr int kScaleRow = 36, kScaleSet = 4 * kScaleRow;
 constexpr int kOffScale = kOffV + kStages * kOperand;        // [slot][k, v][kScaleSet] floats
 constexpr int kOffExp = kOffScale + kSlots * 2 * kScaleSet * 4;  // [slot][4] ints
 constexpr int kOffBar = kOffExp + kSlots * 4 * 4;
-constexpr int kBars = 4 * kStages + kSlots + 2 + 4 + 4 + 2 + 1;
+constexpr int kBars = 4 * kStages + kSlots + 2 + 4 + 4 + 2 + 2 + 1;
 constexpr int kSmem = kOffBar + kBars * 8 + 16 + 1024;
 
 constexpr int kColO = 0, kColS = 256;  // tensor memory columns (tile B: + 128)
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
   uint64_t *k_full = bars, *k_free = k_full + kStages, *v_full = k_free + kStages,
            *v_free = v_full + kStages, *sc_full = v_free + kStages, *q_full = sc_full + kSlots,
-           *s_full = q_full + 2, *p_full = s_full + 4, *o_done = p_full + 4, *last_done = o_done + 2;
+           *s_full = q_full + 2, *p_full = s_full + 4, *o_done = p_full + 4, *o_last = o_done + 2, *last_done = o_last + 2;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hkv = (int)a.Hkv, lgG = pl.lgG;
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], kSoftmaxWarps / 2);
       mbar_init(&o_done[x], 1);
+      mbar_init(&o_last[x], 1);
     }
     for (int x = 0; x < 4; ++x) {  // [row tile][half of the token tile]
       mbar_init(&s_full[x], 1);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
     const int x = warp >> 3, first_row = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
     const uint32_t ts = tmem + ((uint32_t)first_row << 16) + kColS + 128 * x,
                    to = tmem + ((uint32_t)first_row << 16) + kColO + 128 * x;
-    int it = 0, su = 0;  // token tiles of the CTA, half tiles of this row tile
+    int it = 0, su = 0, groups = 0;  // token tiles of the CTA, half tiles and row groups of this row tile
     bool ok = true;
     while (ok && un.next(item, t0, n)) {
       const int j = item / pl.tc_groups;
@@ -335,9 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
       }
       it += n;
       if (!ok) break;
-      // the last two outputs in turn (the scores of a half tell of all but those)
-      ok = wait_warp(&o_done[x], su & 1) && wait_warp(&o_done[x], (su - 1) & 1);
+      // All outputs of the row group, on a barrier that completes once a group: o_done
+      // may be one or two phases on by now, and a wait for the parity of the first of
+      // two that are both complete would wait for a third, which does not come.
+      ok = wait_warp(&o_last[x], groups & 1);
       if (!ok) break;
+      ++groups;
       tc_fence_after();
       const int64_t part = (int64_t)((int)blockIdx.x - tc_first_cta(pl, item)) * rows_out;
       float inv[2];
@@ -519,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
               if (!ok) break;
               tc_fence_after();
               output(x, s, half, i > 0 || half > 0);
+              if (last && half == 1) commit(&o_last[x]);
               ++su[x];
             }
             // products into different columns are not bound to run in order: the scores

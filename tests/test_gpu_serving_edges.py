@@ -40,3 +40,39 @@ def test_prefix_attention_of_many_row_groups(B, L, H, Hkv, P, mode):
     for _ in range(50):
         got = bn.prefix_attention(mode, *a.d)
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+# ----------------------------------------------------------------- weights
+def _check_weights(mode, q, lse, k, acc, lens, got):
+    """test_gpu_serving's bound: each weight off by the score's error and roundings
+    of s - lse and exp2, the sum of R rows by R u of itself."""
+    want = ref.weights(mode, q, lse, k, acc, lens)
+    kv = np.abs(ref.values(mode, k).reshape(-1, 128)).max(0)
+    ds = 2.0 ** -16 * float((np.abs(q.astype(np.float64)).max(axis=(0, 1, 2)) * kv).sum()) / np.sqrt(128)
+    size = 1 + np.abs(lse[np.isfinite(lse)]).max()
+    ds += 2.0 ** -21 * size
+    B, L, H, _ = q.shape
+    rel = 2 * ds + 2.0 ** -20 * size + (B * L * H // k[0].shape[-2] + 2) * 2.0 ** -24
+    assert np.all(np.abs(got - want) <= rel * (want - acc) + 2.0 ** -23 * np.abs(want))
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("B,L,H,Hkv,P", [
+    (224, 4, 8, 8, 2400),   # 7 row tiles; 152 token tiles, 19 a head: runs of one and two, across heads
+    (100, 1, 64, 8, 5003),  # 7 row tiles; 320 token tiles, 40 a head: two or three a CTA
+    (170, 1, 64, 8, 4800),  # 11 row tiles; 304 token tiles, 38 a head
+    (48, 1, 64, 8, 9600)])  # 3 row tiles: one slot is left out of segments of one tile
+def test_weights_of_odd_row_tiles(B, L, H, Hkv, P, mode):
+    """Row tiles that leave a slot out at a segment's end, segments of one token
+    tile in a row: each row's lse is there until the last slot has read it."""
+    rng = np.random.default_rng(P)
+    q = (rng.standard_normal((B, L, H, 128)) * 1.2).astype(np.float16)
+    k = tuple(rng.integers(0, 256, (P, Hkv, 64)).astype(np.uint8) for _ in range(2)) + (
+        (rng.random((P, Hkv)) * 0.2).astype(np.float16),)
+    lse = (rng.standard_normal((B, L, H)) + 20.0).astype(np.float32)
+    acc = rng.random((Hkv, P)).astype(np.float32)
+    d = dev(q), dev(lse), tuple(dev(x) for x in k)
+    first = bn.kv_weights(mode, *d, dev(acc))
+    _check_weights(mode, q, lse, k, acc, None, host(first))
+    for _ in range(20):
+        assert torch.equal(bn.kv_weights(mode, *d, dev(acc)), first)

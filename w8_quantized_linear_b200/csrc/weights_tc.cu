@@ -39,7 +39,7 @@ using namespace tc16;
 
 constexpr int kSms = 148;
 constexpr int kTile = 128;
-constexpr int kSlots = 4, kPair = 2, kStages = 2, kSets = 8;
+constexpr int kSlots = 4, kPair = 2, kStages = 2, kSets = 16;
 constexpr int kSlotWarps = 4 * kSlots, kCodeWarps = 4;
 constexpr int kIssueWarp = kSlotWarps + kCodeWarps, kRowWarp = kIssueWarp + 1;
 constexpr int kThreads = (kRowWarp + 1) * 32;
@@ -49,9 +49,14 @@ constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(1
 
 // A set: -lse log2(e) of a row tile, row 8 n + 2 q + i at q * kSetRow + 2 n + i, the
 // order in which a thread of lane % 4 = q holds its columns, rows in different banks.
-// Eight of them: a set is read by slots whose products come before the one that frees
-// the stage of the row tile six later, and the loader waits for that.
+// The loader writes row tile i's set when the stage of row tile i - kStages is free,
+// that is, when that tile's products are issued.  A slot has read a set when its next
+// product is issued, which is at most 2 kSlots - 1 row tiles later: where a segment of
+// one token tile has 4 n + 3 row tiles, its last round leaves out slot 3, and in the
+// next segment slot 3 comes fourth (a slot that a whole segment leaves out is bound by
+// the barrier at the segment's end).
 constexpr int kSetRow = 36, kSet = 4 * kSetRow;
+static_assert(kSets - kStages >= 2 * kSlots - 1 && (kSets & (kSets - 1)) == 0, "a set is read before it is written");
 constexpr int kOffK = 0;  // [segment % 2][tile]
 constexpr int kOffQ = kOffK + 2 * kPair * kOperand;
 constexpr int kOffSet = kOffQ + kStages * kOperand;

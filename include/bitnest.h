@@ -514,8 +514,8 @@ int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t 
  * D must be 128, H / Hkv one of 1, 2, 4, 8.  The prefix is attended by all
  * B * L * H / Hkv rows of a KV head together; its planes are read once for
  * them, not once for each sequence.  Scores, statistics and sums are fp32; each
- * p * v_scale enters its product rounded to fp16 (2^-11 of it at most), as the
- * output is.  Results do not depend on timing.
+ * p * v_scale enters its product as two fp16 terms (22 bits), and the output
+ * is rounded to fp16.  Results do not depend on timing.
  */
 int64_t bitnest_prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
                                           int64_t cap);

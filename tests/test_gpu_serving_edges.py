@@ -42,6 +42,61 @@ def test_prefix_attention_of_many_row_groups(B, L, H, Hkv, P, mode):
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
 
 
+def _two_kinds(c):
+    """Tokens of two kinds in turn: the first's score is q k = c / sqrt(128) above
+    the second's, their values are 4 and -7 (all codes are the draft's and the
+    target's alike)."""
+    B, L, H, Hkv, P, cap = c.shape
+    q = np.zeros((B, L, H, 128), np.float16)
+    # the second kind's weight e^-x is just above 4 / 7, so outputs nearly cancel, and as
+    # far from a value of 11 bits as one can be there
+    x = np.arange(5.0, 7.5, 2.0 ** -8).astype(np.float16).astype(np.float64)
+    w = np.exp(-x / np.sqrt(128.0))
+    off = np.abs(w.astype(np.float16).astype(np.float64) / w - 1)
+    off[np.abs(7 * w - 4) > 0.1] = 0.0
+    assert off.max() > 0.8 * 2.0 ** -11
+    q[..., 0] = x[off.argmax()]
+    c.q = q
+    first = np.arange(max(P, cap)) % 2 == 0
+
+    def planes(n, rows, value):
+        hi = np.full((n, 64), 0x88, np.uint8)
+        hi[:] = value(first[:n])
+        hi = np.broadcast_to(hi.reshape((1,) * (len(rows) - 2) + (n, 1, 64)), (*rows, 64)).copy()
+        return hi, np.full_like(hi, 0x88), np.ones(rows, np.float16)
+
+    def key(f):
+        out = np.full((len(f), 64), 0x88, np.uint8)
+        out[:, 0] = np.where(f, 0x89, 0x88)  # 1 or 0 in column 0
+        return out
+
+    def val(f):
+        return np.where(f, 0xcc, 0x11).astype(np.uint8)[:, None]
+
+    c.prefix = [planes(P, (P, Hkv), key), planes(P, (P, Hkv), val)] if P else None
+    c.own = [planes(cap, (B, cap, Hkv), key), planes(cap, (B, cap, Hkv), val)] if cap else None
+    c.upload()
+    return c
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("shape", [(64, 1, 8, 1, 512, 0), (1, 1, 8, 1, 512, 0), (2, 1, 8, 1, 512, 0),
+                                   (2, 4, 8, 1, 0, 512), (1, 2, 4, 1, 0, 512)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_prefix_attention_keeps_the_weights_bits(shape, mode):
+    """Outputs that nearly cancel show what the weights p v_scale lose on their way
+    into the product: 2^-11 of them would be 2^-12 of sum p |v| here."""
+    a = _two_kinds(Attend(*shape, [shape[5]] * shape[0]))
+    out, _, size = ref.attention(mode, a.q, a.prefix, a.own, a.lens)
+    got = host(bn.prefix_attention(mode, *a.d)[0]).astype(np.float64)
+    # scores below 1: their roundings and exp2's are below 2^-20 of a weight, two fp16
+    # terms hold it to 2^-22; up to 512 additions off by 2^-23 of the sum of magnitudes;
+    # parts join with a few roundings more; the output's own rounding
+    tol = (512 * 2.0 ** -23 + 2.0 ** -18) * size + 2.0 ** -11 * np.abs(out) + 2.0 ** -25
+    assert np.all(2.0 ** -12.6 * size > 2 * (tol - 2.0 ** -11 * np.abs(out)))  # the loss would show
+    assert np.all(np.abs(got - out) <= tol)
+
+
 # ----------------------------------------------------------------- weights
 def _check_weights(mode, q, lse, k, acc, lens, got):
     """test_gpu_serving's bound: each weight off by the score's error and roundings

@@ -78,6 +78,15 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// v as a sum of two fp16 terms, 22 bits together (v below 2^15, and no less than
+// 2^-25 of it is kept); `lo` is the second.
+__device__ __forceinline__ uint32_t split_half2(float v0, float v1, uint32_t &lo) {
+  const uint32_t hi = pack_half2(v0, v1);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  lo = pack_half2(v0 - h.x, v1 - h.y);
+  return hi;
+}
+
 __device__ __forceinline__ float half_bits(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 
 __device__ __forceinline__ float exp2_approx(float x) {

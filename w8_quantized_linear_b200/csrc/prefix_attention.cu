@@ -107,8 +107,8 @@ struct Loader {
 // r seeing tokens below lim(r).  As on the tcgen05 path p is kept as 2^(s -
 // shift), shift = m + e - kHead with m a maximum at most kSlack behind and 2^e
 // above every V scale so far: the output is rescaled only when one of them has
-// grown, and p v_scale < 2^15 enters the product as one fp16 term (11 bits:
-// 2^-11 of each weight at most, as the fp16 output's own rounding is).
+// grown, and p v_scale < 2^15 enters the product as two fp16 terms (22 bits
+// together; one alone would put 2^-11 of every weight into outputs that cancel).
 // e with vmax < 2^e, at most 100 (an infinite scale)
 __device__ __forceinline__ int e_tile_of(float vmax) {
   return vmax > 0.0f ? min(100, (int)((__float_as_uint(vmax) >> 23) & 0xFFu) - 126) : kMinExp;
@@ -238,7 +238,7 @@ __device__ __forceinline__ void attend(Part<NT> &st, const uint4 *frag, Loader<M
         }
       }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
       float p[4], sum = 0.0f;
@@ -250,8 +250,8 @@ __device__ __forceinline__ void attend(Part<NT> &st, const uint4 *frag, Loader<M
         p[i] = seen ? p[i] * vf[i] : 0.0f;
       }
       l_run[r] += sum;  // this lane's tokens only
-      pb[r][0] = pack_half2(p[0], p[1]);
-      pb[r][1] = pack_half2(p[2], p[3]);
+      pb[r][0] = split_half2(p[0], p[1], pl[r][0]);
+      pb[r][1] = split_half2(p[2], p[3], pl[r][1]);
     }
     uint32_t ev[4][2], od[4][2];
 #pragma unroll
@@ -274,8 +274,10 @@ __device__ __forceinline__ void attend(Part<NT> &st, const uint4 *frag, Loader<M
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           mma_f16(o[2 * h + i][nt], a[0][i], a[1][i], a[2][i], a[3][i], pb[nt][0], pb[nt][1]);
+          mma_f16(o[2 * h + i][nt], a[0][i], a[1][i], a[2][i], a[3][i], pl[nt][0], pl[nt][1]);
+        }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");

@@ -11,8 +11,8 @@
 //          row (so that a token's scales serve two rows of a thread, and a
 //          thread needs a quarter of them): the scores from tensor memory,
 //          times the tokens' K scales, the row's running maximum,
-//          p = 2^(s - shift), times the V scales, rounded to fp16 and written
-//          back over the scores as the second product's A operand;
+//          p = 2^(s - shift), times the V scales, written back over the
+//          scores as the second product's A operand, in two fp16 terms;
 //   16-23  the cache's codes as fp16 operands: plane words -> shared memory
 //          (128-byte swizzle), two stages of K and of V; the tokens' scales;
 //   24     issues the MMAs.
@@ -31,7 +31,9 @@
 // V scale has (the softmax warps do it in place): p is kept as 2^(s - shift)
 // with shift = m + e - 7, m a maximum that is at most 8 behind, 2^e above every
 // V scale so far, so p v_scale < 2^15 in fp16, with 2^29 between it and fp16's
-// subnormals; row sums carry the same factor, which cancels.
+// subnormals; row sums carry the same factor, which cancels.  p v_scale enters the
+// product as two fp16 terms, 22 bits together: one alone would put 2^-11 of every
+// weight into outputs that cancel.
 //
 // Columns of a head are kept in the order 0 2 4 6 1 3 5 7 within each 8 (the
 // order in which plane words unpack with the fewest instructions): the same
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
             st_16x8(to + 8 * c, o);
           }
         }
-        uint32_t pk[16];
+        uint32_t pk[16], pl[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float *p = t + 8 * k;
@@ -325,10 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
             p[q + 1] = exp2_approx(p[q + 1]);
             f32x2_add(sum[r][0], sum[r][1], sum[r][0], sum[r][1], p[q], p[q + 1]);
             f32x2_mul(p[q], p[q + 1], p[q], p[q + 1], q < 4 ? v4.x : v4.z, q < 4 ? v4.y : v4.w);
-            pk[4 * k + q / 2] = pack_half2(p[q], p[q + 1]);
+            pk[4 * k + q / 2] = split_half2(p[q], p[q + 1], pl[4 * k + q / 2]);
           }
         }
+        // over the scores (all read): the first terms, the second ones behind them
         st_16x32(th, pk);
+        st_16x32(th + kHalf / 2, pl);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -480,13 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixAttnArgs a
         __syncwarp();
         issued = true;
       };
-      // O_x += P_x V for a half: 4 k-steps of 16 tokens
+      // O_x += P_x V for a half: 4 k-steps of 16 tokens of each of the weights' two terms
       auto output = [&](int x, int s, int half, bool add) {
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
             mma_ts(tmem + kColO + 128 * x, tmem + kColS + 128 * x + kHalf * half + 8 * k,
-                   vd + s * kOp + (2048 >> 4) * (4 * half + k), idesc(true, kD), add || k > 0);
+                   vd + s * kOp + (2048 >> 4) * (4 * half + (k & 3)), idesc(true, kD), add || k > 0);
           umma_commit(&o_done[x]);
         }
         __syncwarp();

@@ -25,6 +25,42 @@ def _no_wait_timeouts():
     assert bn.device_wait_timeout(reset=True) == 0
 
 
+# ------------------------------------------------------------------ rotary
+@pytest.mark.parametrize("layout", [bn.ROPE_HALF, bn.ROPE_PAIRS])
+@pytest.mark.parametrize("src,dst", [("f16", "f16"), ("f16", "f32"), ("f32", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("D,rot", [(128, 64), (80, 32), (128, 8), (24, 16), (96, 96)])
+def test_rope_at_any_element(D, rot, src, dst, layout):
+    """x and y at any element of a wider array, heads that turn in part: only the
+    element type's alignment is asked for.  The same bits as from an aligned array,
+    which test_gpu_serving holds against the oracle; what lies beside stays."""
+    types = {"f16": torch.float16, "f32": torch.float32}
+    M, heads = 5, 3
+    rng = np.random.default_rng(D + rot)
+    row = heads * D + 16
+    base = dev(rng.standard_normal((M, row)).astype(np.float32)).to(types[src])
+    pos = dev(rng.integers(0, 9000, M).astype(np.int32))
+    phases, mag = bn.rope_phases(rot, 1e4)
+
+    def view(wide, first):
+        return wide[:, first:first + heads * D].unflatten(1, (heads, D))
+
+    for first in (0, 1, 2, 4, 6, 8, 12):
+        x = view(base, first)
+        want = bn.rope(x.contiguous(), pos, phases, mag, layout, dtype=types[dst])
+        assert torch.equal(bn.rope(x, pos, phases, mag, layout, dtype=types[dst]), want)
+        for to in (0, 1, 2, 4, 6):
+            wide = torch.full((M, row), 7.0, dtype=types[dst], device="cuda")
+            bn.rope(x, pos, phases, mag, layout, out=view(wide, to))
+            assert torch.equal(view(wide, to), want)
+            assert torch.all(wide[:, :to] == 7.0) and torch.all(wide[:, to + heads * D:] == 7.0)
+        if src == dst:
+            wide = base.clone()
+            bn.rope(view(wide, first), pos, phases, mag, layout, out=view(wide, first))
+            assert torch.equal(view(wide, first), want)
+            assert torch.equal(wide[:, :first], base[:, :first])
+            assert torch.equal(wide[:, first + heads * D:], base[:, first + heads * D:])
+
+
 # --------------------------------------------------------------- attention
 @pytest.mark.parametrize("mode", [0, 1])
 @pytest.mark.parametrize("B,L,H,Hkv,P", [

@@ -144,8 +144,7 @@ struct Raw {
 // ------------------------------------------------------------------- rope
 // A thread owns V pairs of one token (2 V values: two runs of V in the halves
 // layout, one run of 2 V of adjacent pairs) and goes over `per` heads with
-// the same cosines and sines; the values behind `rot` are copied in runs of
-// 2 V.  Every value is read and written by one thread, so x may be y.
+// the same cosines and sines; the values behind `rot` are copied 2 V a thread.  Every value is read and written by one thread, so x may be y.
 template <typename TX, typename TY, int V, bool PAIRS>
 __global__ void __launch_bounds__(256) rope_kernel(
     const TX *__restrict__ x, int64_t x_token, int64_t x_head, TY *__restrict__ y, int64_t y_token,
@@ -253,9 +252,14 @@ __global__ void __launch_bounds__(256) rope_kernel(
     } else {
       for (int h = hg * per; h < h_end; ++h, xp += x_head, yp += y_head) {
         if constexpr (V > 1) {
-          float v[2 * V];
-          load_vec<TX, 2 * V>(xp + at, v);
-          store_vec<TY, 2 * V>(yp + at, v);
+          // in the runs of the turned values, whose alignment was asked for
+          constexpr int kRun = PAIRS ? 2 * V : V;
+#pragma unroll
+          for (int r = 0; r < 2 * V; r += kRun) {
+            float v[kRun];
+            load_vec<TX, kRun>(xp + at + r, v);
+            store_vec<TY, kRun>(yp + at + r, v);
+          }
         } else {
           for (int i = at; i < min(D, at + 2); ++i) {
             float v[1];
@@ -289,7 +293,9 @@ cudaError_t launch_rope_v(const RopeArgs &a, cudaStream_t st) {
 }
 
 // 8 or 4 pairs a thread where the lengths, strides and addresses allow its
-// loads and stores, else one.
+// loads and stores, else one.  No access is wider than a run of turned values or
+// 16 bytes, and every one starts a multiple of V (2 V for pairs) values into a
+// head: what `fits` asks of the addresses covers them all.
 template <typename TX, typename TY>
 cudaError_t launch_rope_t(const RopeArgs &a, cudaStream_t st) {
   auto fits = [&](int V) {

@@ -61,6 +61,20 @@ def test_rope_at_any_element(D, rot, src, dst, layout):
             assert torch.equal(wide[:, first + heads * D:], base[:, first + heads * D:])
 
 
+@pytest.mark.parametrize("layout", [bn.ROPE_HALF, bn.ROPE_PAIRS])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (80, 40)])
+def test_rope_in_place_of_many_tokens(D, rot, dtype, layout):
+    """Several heads a thread, x and y the same array: the bits of another array."""
+    M, heads = 3001, 32
+    x = torch.randn((M, heads, D), generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")
+    phases, mag = bn.rope_phases(rot, 1e4)
+    want = bn.rope(x, pos, phases, mag, layout, dtype=dtype)
+    assert bn.rope(x, pos, phases, mag, layout, out=x) is x
+    assert torch.equal(x, want)
+
+
 # --------------------------------------------------------------- attention
 @pytest.mark.parametrize("mode", [0, 1])
 @pytest.mark.parametrize("B,L,H,Hkv,P", [

@@ -29,15 +29,23 @@ __device__ __forceinline__ void turn(uint64_t phase, int32_t pos, float sign, fl
   s *= mag * sign;
 }
 
+// Plain loads where the array may be written by the same kernel (rope in place), the
+// read-only path elsewhere.
+template <bool RO, typename U>
+__device__ __forceinline__ U load(const U *p) {
+  if constexpr (RO) return __ldg(p);
+  return *p;
+}
+
 // N consecutive values of type T as fp32, by loads of up to 16 bytes.
-template <typename T, int N>
+template <bool RO, typename T, int N>
 __device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
   constexpr int kBytes = sizeof(T) * N;
   if constexpr (sizeof(T) == 4) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
+        const float4 f = load<RO>(reinterpret_cast<const float4 *>(p) + i);
         v[4 * i] = f.x;
         v[4 * i + 1] = f.y;
         v[4 * i + 2] = f.z;
@@ -45,14 +53,14 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
+      for (int i = 0; i < N; ++i) v[i] = load<RO>(p + i);
     }
   } else if constexpr (kBytes % 8 == 0) {
     uint32_t w[N / 2];
     if constexpr (kBytes % 16 == 0) {
 #pragma unroll
       for (int i = 0; i < N / 8; ++i) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        const uint4 u = load<RO>(reinterpret_cast<const uint4 *>(p) + i);
         w[4 * i] = u.x;
         w[4 * i + 1] = u.y;
         w[4 * i + 2] = u.z;
@@ -61,7 +69,7 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
     } else {
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+        const uint2 u = load<RO>(reinterpret_cast<const uint2 *>(p) + i);
         w[2 * i] = u.x;
         w[2 * i + 1] = u.y;
       }
@@ -121,7 +129,7 @@ struct Raw {
   uint4 w[kPieces];
   __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    for (int i = 0; i < kPieces; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
   }
   __device__ __forceinline__ void get(float (&v)[N]) const {
 #pragma unroll
@@ -144,11 +152,12 @@ struct Raw {
 // ------------------------------------------------------------------- rope
 // A thread owns V pairs of one token (2 V values: two runs of V in the halves
 // layout, one run of 2 V of adjacent pairs) and goes over `per` heads with
-// the same cosines and sines; the values behind `rot` are copied 2 V a thread.  Every value is read and written by one thread, so x may be y.
+// the same cosines and sines; the values behind `rot` are copied 2 V a thread.
+// Every value is read, by plain loads, and written by one thread, so x may be y.
 template <typename TX, typename TY, int V, bool PAIRS>
 __global__ void __launch_bounds__(256) rope_kernel(
-    const TX *__restrict__ x, int64_t x_token, int64_t x_head, TY *__restrict__ y, int64_t y_token,
-    int64_t y_head, const int32_t *__restrict__ pos, const uint64_t *__restrict__ phase, float mag,
+    const TX *x, int64_t x_token, int64_t x_head, TY *y, int64_t y_token, int64_t y_head,
+    const int32_t *__restrict__ pos, const uint64_t *__restrict__ phase, float mag,
     float sign, int64_t M, int heads, int D, int rot, int per) {
   const int turned = rot / (2 * V);                            // units of a head that turn
   const int units = turned + (D - rot + 2 * V - 1) / (2 * V);  // and all of them
@@ -222,12 +231,12 @@ __global__ void __launch_bounds__(256) rope_kernel(
         float a[V], b[V];
         if constexpr (PAIRS) {
           float v[2 * V];
-          load_vec<TX, 2 * V>(xp + 2 * V * u, v);
+          load_vec<false, TX, 2 * V>(xp + 2 * V * u, v);
 #pragma unroll
           for (int i = 0; i < V; ++i) a[i] = v[2 * i], b[i] = v[2 * i + 1];
         } else {
-          load_vec<TX, V>(xp + V * u, a);
-          load_vec<TX, V>(xp + rot / 2 + V * u, b);
+          load_vec<false, TX, V>(xp + V * u, a);
+          load_vec<false, TX, V>(xp + rot / 2 + V * u, b);
         }
         turn_head(a, b, yp);
       }
@@ -257,13 +266,13 @@ __global__ void __launch_bounds__(256) rope_kernel(
 #pragma unroll
           for (int r = 0; r < 2 * V; r += kRun) {
             float v[kRun];
-            load_vec<TX, kRun>(xp + at + r, v);
+            load_vec<false, TX, kRun>(xp + at + r, v);
             store_vec<TY, kRun>(yp + at + r, v);
           }
         } else {
           for (int i = at; i < min(D, at + 2); ++i) {
             float v[1];
-            load_vec<TX, 1>(xp + i, v);
+            load_vec<false, TX, 1>(xp + i, v);
             store_vec<TY, 1>(yp + i, v);
           }
         }
@@ -446,8 +455,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a, int per) {
       if (live && h + n < h_end) {
         const T *p = src + (int64_t)(h + n) * kD;
         float x[4], y[4];
-        load_vec<T, 4>(p + c0, x);
-        load_vec<T, 4>(p + c1, y);
+        load_vec<true, T, 4>(p + c0, x);
+        load_vec<true, T, 4>(p + c1, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[n][i] = x[i], v[n][4 + i] = y[i];
       } else {

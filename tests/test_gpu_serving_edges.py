@@ -92,6 +92,20 @@ def test_prefix_attention_of_many_row_groups(B, L, H, Hkv, P, mode):
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
 
 
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("B,L,H,Hkv,P,cap", [
+    (1, 2, 8, 1, 700, 0), (2, 2, 8, 1, 700, 0), (8, 1, 8, 1, 700, 0),  # eight, four and two warps a row
+    (8, 2, 8, 1, 900, 0), (8, 2, 8, 1, 0, 900)])                       # one; own tokens: eight
+def test_prefix_attention_joins_a_ctas_warps(B, L, H, Hkv, P, cap, mode):
+    """The states of a CTA's warps that share rows, call after call."""
+    a = Attend(B, L, H, Hkv, P, cap, [cap - 100 * i * (cap > 0) for i in range(B)])
+    first = bn.prefix_attention(mode, *a.d)
+    a.check(mode, first)
+    for _ in range(50):
+        got = bn.prefix_attention(mode, *a.d)
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
 def _two_kinds(c):
     """Tokens of two kinds in turn: the first's score is q k = c / sqrt(128) above
     the second's, their values are 4 and -7 (all codes are the draft's and the

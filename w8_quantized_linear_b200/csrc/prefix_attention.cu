@@ -390,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
   store_state(sh, st, warp, lane);
   __syncthreads();
   // the warps' states joined by rows' factors 2^(shift_w - M) / den (0 for a
-  // warp that saw no token; NaN scores make l NaN)
-  {
-    const int t = threadIdx.x & 127, k = t & (ways - 1), row = t / ways;  // 128 = rows x ways
+  // warp that saw no token; NaN scores make l NaN): 128 rows x ways, a thread each of
+  // the first four warps
+  if (warp < 4) {
+    const int t = threadIdx.x, k = t & (ways - 1), row = t / ways;
     const int w = row / kRows + k * row_warps, rr = row % kRows, r = row0 + row;
     const bool in = rr < 8 * NT;
     const float l = in ? sh.l[w][rr] : 0.0f, m = in ? sh.m[w][rr] : 0.0f;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) parts_kernel(PrefixAttnArgs a, Pl
     float den = f * l;
     for (int x = 1; x < ways; x <<= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
     __syncwarp();
-    if (threadIdx.x < 128 && in) {
+    if (in) {
       sh.m[w][rr] = den == 0.0f ? 0.0f : f / den;
       if (k == 0 && r < R)
         part_lse[(int64_t)part * rows_out + query_row(bi0, r, lgG, H, j)] =

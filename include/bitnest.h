@@ -534,7 +534,8 @@ int bitnest_prefix_attention(int mode, const uint16_t *q, int64_t B, int64_t L, 
  *                    [cap, Hkv, 64], acc fp32 [Hkv, cap]), the prefix.
  *   q, lse         : bitnest_prefix_attention's; a query with lse = -inf gives
  *                    no weight.  Values of acc at or past len[b] are left.
- * B * Hkv <= 65535 where len is given.  Sums are fp32, in a fixed order.
+ * B * Hkv <= 65535 where len is given, Hkv * ceil(cap / 128) < 2^30 where it is
+ * not.  Sums are fp32, in a fixed order.
  */
 int bitnest_kv_weights(int mode, const uint16_t *q, const float *lse, int64_t B, int64_t L,
                        int64_t H, int64_t Hkv, int64_t D, const uint8_t *k_hi, const uint8_t *k_lo,

@@ -193,3 +193,13 @@ def test_oracle_evict_by_hand():
     assert ref.evict(acc, 8, 4, 2, 1) == [0, 1, 2, 7]  # of the three fives the first
     acc[2] = np.nan
     assert ref.evict(acc, 8, 3, 0, 0) == [0, 3, 5] and ref.evict(acc, 7, 6, 1, 0) == [0, 1, 3, 4, 5, 6]
+
+
+def test_weights_refuses_more_tiles_of_a_shared_cache_than_it_counts(L):
+    def call(Hkv, cap, lens=None):
+        return L.bitnest_kv_weights(1, A, A, 1, 1, Hkv, Hkv, 128, A, A, A, cap, lens, A + 1, None)
+
+    # (the misaligned acc ends the calls whose shape is taken)
+    assert call(128, 1 << 30) == 2 and call(129, 1 << 30) == 2 and call(127, 1 << 30) == 3
+    assert call(65535, 16384 * 128) == 3 and call(65535, 16385 * 128) == 2  # 2^30 - 2^14 tiles, and 65535 more
+    assert call(128, 1 << 30, lens=A) == 3  # own tokens: another kernel

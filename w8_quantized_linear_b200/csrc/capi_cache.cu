@@ -209,7 +209,8 @@ int bitnest_kv_weights(int mode, const uint16_t *q, const float *lse, int64_t B,
                        void *stream) {
   if (mode != BITNEST_DRAFT && mode != BITNEST_TARGET) return BITNEST_ERR_INVALID_ARG;
   if (D != 128 || L < 1 || !heads_ok(H, Hkv) || !cache_shape_ok(B, cap, Hkv) || L > kMost ||
-      (B > 0 && B * L > kMost / H) || (len && B * Hkv > 65535))
+      (B > 0 && B * L > kMost / H) || (len && B * Hkv > 65535) ||
+      (!len && Hkv * ((cap + 127) / 128) > 0x3fffffff))  // token tiles, counted in 32 bits
     return BITNEST_ERR_UNSUPPORTED_SHAPE;
   if (B == 0 || cap == 0) return BITNEST_OK;
   const bool lo = mode == BITNEST_TARGET;

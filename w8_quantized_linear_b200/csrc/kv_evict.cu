@@ -16,8 +16,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kScale = 0.088388347648318440550f * kLog2e;  // log2(e) / sqrt(128)
 
 // ---------------------------------------------------------------- weights
-// For more than 128 rows of one sequence's KV head (else few_rows_kernel below,
-// or weights_tc.cu):
+// For more than 128 rows of one sequence's KV head and its own tokens (else
+// few_rows_kernel below; a shared prefix of many rows: weights_tc.cu):
 // acc[t] += sum over the rows (queries x heads of the KV head) that see token
 // t of exp(q k_t / sqrt(128) - lse): the scores once more, from the K planes
 // alone, with no maximum to keep since lse is known.  A warp holds the codes
@@ -33,11 +33,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
   const int gid = lane >> 2, tig = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
-  const bool own = a.len != nullptr;
   const int j = (int)(blockIdx.y % a.Hkv);
-  const int64_t b = blockIdx.y / a.Hkv;  // 0 where the cache is shared
-  const int len = own ? (int)min((int64_t)a.len[b], a.cap) : (int)a.cap;
-  const int R = (int)(own ? a.L : a.B * a.L) << lgG;
+  const int64_t b = blockIdx.y / a.Hkv;
+  const int len = (int)min((int64_t)a.len[b], a.cap);
+  const int R = (int)a.L << lgG;
   const int bi0 = (int)(b * a.L);
   const int tw = warp / ways, way = warp % ways;  // token group of the CTA, share of the rows
   const int t0 = (blockIdx.x * (kWarps / ways) + tw) * kTokens;
@@ -86,9 +85,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) weights_kernel(KvWeightsArgs a
       const float e1 = r1 < R ? __ldg(a.lse + at1) : -INFINITY;
       const float b0 = e0 == -INFINITY ? INFINITY : e0 * kLog2e;
       const float b1 = e1 == -INFINITY ? INFINITY : e1 * kLog2e;
-      // own tokens: query i sees those below len - L + 1 + i
-      const int lim0 = own ? len - (int)a.L + 1 + (r0 >> lgG) : len;
-      const int lim1 = own ? len - (int)a.L + 1 + (r1 >> lgG) : len;
+      // query i sees the tokens below len - L + 1 + i
+      const int lim0 = len - (int)a.L + 1 + (r0 >> lgG);
+      const int lim1 = len - (int)a.L + 1 + (r1 >> lgG);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -577,8 +576,7 @@ constexpr int64_t kTcRows = 128;
 cudaError_t launch_kv_weights(const KvWeightsArgs &a, cudaStream_t st) {
   const int G = (int)(a.H / a.Hkv);
   const int64_t R = (a.len ? a.L : a.B * a.L) * G;
-  if (!a.len && R >= kTcRows && a.Hkv * ((a.cap + 127) / 128) <= 0x3fffffff)
-    return evict::launch_weights_tc(a, st);
+  if (!a.len && R >= kTcRows) return evict::launch_weights_tc(a, st);
   int lgG = 0;
   while ((1 << lgG) < G) ++lgG;
   const int64_t caches = (a.len ? a.B : 1) * a.Hkv;

@@ -31,8 +31,6 @@ ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = range(5)
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbitnest.so")
 
-BINDING_PATH = os.path.join(_HERE, "_binding.so")
-
 _lib = None
 _binding = None
 
@@ -392,17 +390,21 @@ class _KvCacheC(ctypes.Structure):
 
 
 def _serving():
-    """The calls below on tensors (_binding.so, built in-tree by build.py)."""
+    """The calls below on tensors (_binding.*.so, built in-tree by build.py for this
+    Python and this torch)."""
     global _binding
     if _binding is None:
         import importlib.util
 
-        import torch  # noqa: F401  (its libraries, which the binding uses)
+        import torch  # (its libraries, which the binding uses)
 
-        if not os.path.exists(BINDING_PATH):
+        from .build import binding_path
+
+        path = binding_path(torch.__version__)
+        if not os.path.exists(path):
             raise ImportError(
-                f"{BINDING_PATH} is missing: build it with `python -m w8_quantized_linear_b200.build`")
-        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+                f"{path} is missing: build it with `python -m w8_quantized_linear_b200.build`")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.open(tuple(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in m.names),

@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+import test_gpu_serving  # noqa: E402
 from test_gpu_parity import dev, host  # noqa: E402
 from test_gpu_serving import Attend  # noqa: E402
 
@@ -195,3 +196,33 @@ def test_weights_of_odd_row_tiles(B, L, H, Hkv, P, mode):
     _check_weights(mode, q, lse, k, acc, None, host(first))
     for _ in range(20):
         assert torch.equal(bn.kv_weights(mode, *d, dev(acc)), first)
+
+
+# ---------------------------------------------------------------- eviction
+@pytest.mark.parametrize("B,Hkv,cap,keep,sinks,recent,lens", [
+    (2, 2, 8193, 4000, 4, 64, [8193, 8000]),            # rows of 8 spans, held
+    (2, 2, 32768, 18000, 4, 1024, [32768, 20001]),      # ... all of them full
+    (2, 2, 32769, 18000, 0, 0, [32769, 32768]),         # two chunks, the second of one token
+    (1, 2, 70001, 10000, 4, 100, [70001]),              # three chunks, the choice in the top third
+    (2, 2, 70001, 38500, 4, 100, [70001, 65537]),       # of three weights: ties run out in the second chunk
+    (1, 2, 70001, 45800, 4, 100, [70001]),              # ... in the third
+    (1, 1, 70001, 66000, 0, 0, [70001])])               # ... among the least
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+def test_evict_of_long_rows_matches_oracle(B, Hkv, cap, keep, sinks, recent, lens, kind):
+    """Rows of one chunk that stay in registers, and of several that are read again
+    in each round, with ties carried from chunk to chunk; row addresses that are
+    not 16-byte aligned."""
+    test_gpu_serving.test_evict_matches_oracle(B, Hkv, cap, keep, sinks, recent, lens, kind)
+
+
+def test_evict_ties_run_out_in_each_chunk():
+    """Equal weights but for a few: the first of them are kept, up to any place."""
+    n, rng = 70001, np.random.default_rng(0)
+    acc = np.full((1, 1, n), 2.0, np.float32)
+    acc[0, 0, rng.integers(0, n, 500)] = 3.0
+    acc[0, 0, rng.integers(0, n, 500)] = 1.0
+    src, lens = bn.nested_cache(n, 1, 1), dev(np.array([n], np.int32))
+    for keep in (700, 32000, 33000, 65400, 66100, 69900):
+        kept, _ = bn.kv_evict(dev(acc), lens, keep, 2, 3, *src, *bn.nested_cache(keep, 1, 1),
+                              torch.zeros(1, 1, keep, device="cuda"))
+        assert host(kept)[0, 0].tolist() == ref.evict(acc[0, 0], n, keep, 2, 3)

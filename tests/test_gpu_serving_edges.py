@@ -1,6 +1,10 @@
 """GPU: the serving calls at the borders of their kernels: alignments, runs that
 end inside a row group, long caches, rounding, and no bounded wait that gives up.
 The checks and their bounds are test_gpu_serving's."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -226,3 +230,49 @@ def test_evict_ties_run_out_in_each_chunk():
         kept, _ = bn.kv_evict(dev(acc), lens, keep, 2, 3, *src, *bn.nested_cache(keep, 1, 1),
                               torch.zeros(1, 1, keep, device="cuda"))
         assert host(kept)[0, 0].tolist() == ref.evict(acc[0, 0], n, keep, 2, 3)
+
+
+# ----------------------------------------------------------------- capture
+_FIRST = """
+import torch, w8_quantized_linear_b200 as bn
+B, L, H, Hkv, P, cap = 70, 2, 8, 2, 3000, 40
+d = dict(device="cuda")
+x = torch.randn(B * L, H + 2 * Hkv, 128, **d)
+pos = torch.arange(B * L, dtype=torch.int32, **d)
+phases, mag = bn.rope_phases(128, 1e4)
+prefix, own, out = bn.nested_cache(P, Hkv), bn.nested_cache(cap, Hkv, B), bn.nested_cache(16, Hkv, B)
+fill = torch.randn(1, P, 2 * Hkv, 128, **d)
+zero, lens = torch.zeros(B, dtype=torch.int32, **d), torch.full((B,), 30, dtype=torch.int32, **d)
+accs = lambda: (torch.zeros(Hkv, P, **d), torch.zeros(B, Hkv, cap, **d), torch.zeros(B, Hkv, 16, **d))
+acc = accs()
+
+def step():
+    q = bn.rope(x[:, :H], pos, phases, mag).view(B, L, H, 128)
+    kv = x.view(B, L, -1, 128)
+    bn.kv_append(kv[:, :, H:H + Hkv], kv[:, :, H + Hkv:], zero, *own, pos=pos.view(B, L), phases=phases)
+    one = tuple(tuple(t[None] for t in c) for c in prefix)
+    bn.kv_append(fill[:, :, :Hkv], fill[:, :, Hkv:], zero[:1], *one)
+    o, lse = bn.prefix_attention(bn.TARGET, q, prefix, own, lens)
+    bn.kv_weights(bn.TARGET, q, lse, prefix[0], acc[0])
+    bn.kv_weights(bn.TARGET, q, lse, own[0], acc[1], lens)
+    kept, n = bn.kv_evict(acc[1], lens, 10, 1, 2, *own, *out, acc[2])
+    return (o, lse, kept, n, *acc, *bn.kv_read(bn.TARGET, None, cap, *own))
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    r = step()
+graph.replay()
+got = [t.clone() for t in r]
+acc = accs()
+assert all(torch.equal(a, b) for a, b in zip(got, step())) and bool(got[0].abs().max() > 0)
+torch.cuda.synchronize()
+assert bn.device_wait_timeout() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """A graph that holds the first calls a process makes, replayed: the bits of plain calls."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]

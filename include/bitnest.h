@@ -386,6 +386,12 @@ int bitnest_spec_greedy(const bitnest_spec_model *model, int steps, int32_t *seq
 /* ------------------------------------------------------------------------
  * Rotary positions, and serving from a nested KV cache: a batch of sequences
  * that share a prefix, with bounded caches.
+ *
+ * bitnest_prefix_attention and bitnest_kv_weights of many rows wait on the
+ * device for their own copies and products; every wait is bounded.  Should one
+ * run out, the kernel returns with parts of out and lse, or of acc, not
+ * written, the call's status is long since BITNEST_OK, and
+ * bitnest_device_wait_timeout reports it.
  * ---------------------------------------------------------------------- */
 
 /* Types of float arrays where an entry point takes both. */

@@ -18,6 +18,15 @@ if not torch.cuda.is_available():  # pragma: no cover
 
 from test_gpu_parity import dev, host  # noqa: E402
 
+
+@pytest.fixture(autouse=True)
+def _no_wait_timeouts():
+    bn.device_wait_timeout(reset=True)
+    yield
+    torch.cuda.synchronize()
+    assert bn.device_wait_timeout(reset=True) == 0
+
+
 U, HALF = 2.0 ** -24, 2.0 ** -11
 LAYOUT = {"half": bn.ROPE_HALF, "pairs": bn.ROPE_PAIRS}
 DTYPE = {"f16": torch.float16, "f32": torch.float32}

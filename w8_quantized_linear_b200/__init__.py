@@ -385,6 +385,7 @@ def spec_greedy(model: SpecModel, steps: int, seq, length, stats, work):
 # returns them, shaped [B, cap, Hkv, 64] and [B, cap, Hkv] (a shared prefix
 # without the B): `nested_cache` makes an empty one.  These calls run on the
 # current stream of the tensors' device, which need not be the current device.
+# A bounded device wait of theirs that gave up shows in device_wait_timeout only.
 class _KvCacheC(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_hi", "k_lo", "k_scale", "v_hi", "v_lo", "v_scale")]
 

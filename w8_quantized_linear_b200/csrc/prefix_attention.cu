@@ -571,7 +571,7 @@ bool make_plan(Plan &p, int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
   while ((1 << p.lgG) < p.G) ++p.lgG;
   const int64_t most = 0x3fffffff;
   const int64_t R = B * L * p.G;
-  p.tc = P > 0 && R >= kTcMinRows && Hkv * ((R + 15) / 16) * ((P + 15) / 16) > kTcMinTiles;
+  p.tc = P > 0 && R >= kTcMinRows && Hkv * ((R + 15) / 16) * ((P + 15) / 16) >= kTcMinTiles;
   if (p.tc) {
     const int64_t tiles = (P + kTcTokens - 1) / kTcTokens, halves = (R + kTcTile - 1) / kTcTile;
     p.tc_rows = Hkv * halves * tiles <= kSms ? kTcTile : 2 * kTcTile;
@@ -603,7 +603,7 @@ bool make_plan(Plan &p, int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
   if (cap > 0) {
     // One CTA an SM with few tokens each, four with more (two at a time: lengths
     // differ): three tiles a warp.  74 caches of 0 to 3001 tokens beside their prefix
-    // 31.4 us (33.5 with two CTAs an SM and four tiles a warp), 128 of 0 to 1024 the same.
+    // 31.5 us (33.7 with two CTAs an SM and four tiles a warp), 128 of 0 to 1024 the same.
     const int64_t step = kTile * kWarps, base = B * Hkv * p.o_tiles;
     int64_t s = max((kSms + base - 1) / base, min((4 * kSms + base - 1) / base, cap / (3 * step)));
     s = max((int64_t)1, min(s, (cap + step - 1) / step));

@@ -9,16 +9,16 @@ namespace pattn {
 constexpr int kSms = 148;
 constexpr int kTcTile = 128, kTcTokens = 128;  // rows of an MMA tile, tokens of a unit on the tcgen05 path
 // The tcgen05 path from 64 rows of a KV head on, but for little work: with one
-// KV head and 512 tokens the mma.sync path takes 8.6 us with 64 rows and 11.4
-// with 256 against 10.2 and 14.8; at 64 rows and 2048 tokens 10.5 against 10.6,
-// with 8 KV heads 13.1 against 13.6, and at 8192 tokens 25 against 21.
+// KV head, 512 tokens and 64 rows the mma.sync path takes 9.7 us against 9.9, with
+// 256 rows 11.2 against 11.0; at 64 rows and 2048 tokens 11.2 against 10.2, with 8
+// KV heads 14.5 against 12.1, and at 8192 tokens 30 against 20 (join included).
 constexpr int64_t kTcMinRows = 64, kTcMinTiles = 512;  // ... tiles of 16 rows x 16 tokens
 
 struct Plan {
   int G, lgG;           // query heads of a KV head, and their logarithm
   // the prefix on the tensor cores' tcgen05 path: units of (tc_rows rows of a KV
   // head, 128 tokens), dealt to the CTAs in runs; tc_rows is 256, or 128 where
-  // that still gives each CTA one unit (11.4 us instead of 14.8 at 256 rows, 512
+  // that still gives each CTA one unit (11.0 us instead of 14.6 at 256 rows, 512
   // tokens and one KV head)
   bool tc;
   int tc_rows;

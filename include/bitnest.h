@@ -506,9 +506,10 @@ int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t 
  * own cache's last L tokens:  out = sum_t p_t v_t,
  * p = softmax(q k_t / sqrt(128)) with the draft's or the target's values.
  *   q, out         : fp16 [B, L, H, 128]; head h reads KV head h / (H / Hkv).
- *   len            : int32 [B] device, own tokens (at most cap are read).  A
- *                    negative one leaves that sequence's out and lse as they
- *                    were.  A query that sees nothing gets zeros and -inf.
+ *   len            : int32 [B] device, own tokens (more than cap count as
+ *                    cap).  A negative one leaves that sequence's out and lse
+ *                    as they were.  A query that sees nothing gets zeros and
+ *                    -inf.
  *   lse            : fp32 [B, L, H], log sum_t exp(q k_t / sqrt(128)); or NULL.
  *   prefix, own    : the lo planes are read for TARGET only; a cache of no
  *                    tokens (P = 0, cap = 0) may be NULL.  Rows at or past
@@ -517,7 +518,10 @@ int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t 
  *                    (BITNEST_ERR_INVALID_ARG if fewer), 16-byte aligned; its
  *                    contents do not matter.  Calls that run at the same time
  *                    need scratch of their own (two graphs too, if they may).
- * D must be 128, H / Hkv one of 1, 2, 4, 8.  The prefix is attended by all
+ * D must be 128, H / Hkv one of 1, 2, 4, 8; scores |q k_t| / sqrt(128) below
+ * 2^22.  Made for the L of decoding (one token, or a draft's few dozen): any L
+ * is right, but own tokens are read once for each 16 rows (L H / Hkv of them),
+ * so a whole prompt's own attention is far from fast here.  The prefix is attended by all
  * B * L * H / Hkv rows of a KV head together; its planes are read once for
  * them, not once for each sequence.  Scores, statistics and sums are fp32; each
  * p * v_scale enters its product as two fp16 terms (22 bits), and the output
@@ -535,7 +539,8 @@ int bitnest_prefix_attention(int mode, const uint16_t *q, int64_t B, int64_t L, 
  *   acc[b, j, t] += sum over queries i and heads h of KV head j that see token
  *                   t of exp(q k_t / sqrt(128) - lse[b, i, h]).
  *   len given      : each sequence's own cache (planes [B, cap, Hkv, 64], acc
- *                    fp32 [B, Hkv, cap]); query i sees t <= len[b] - L + i.
+ *                    fp32 [B, Hkv, cap]); query i sees t <= len[b] - L + i
+ *                    (a len past cap counts as cap).
  *   len NULL       : one cache that all sequences see whole (planes
  *                    [cap, Hkv, 64], acc fp32 [Hkv, cap]), the prefix.
  *   q, lse         : bitnest_prefix_attention's; a query with lse = -inf gives

@@ -10,10 +10,11 @@
 // batch together, as one product per KV head, and each sequence's own tokens
 // by its rows only; a second kernel joins the parts.
 //
-// Bound of the parts on mma.sync: instructions (some 450 for a warp's 16 tokens
-// x 16 rows, half of them unpacking codes) and, in small calls, latency: 2
-// queries over 2048 + 128 draft tokens take 3.5 us of parts and 2 of the join,
-// 16 x 8 caches of 0 to 1024 target tokens 12 us (17 MB, 2.6 us to read).
+// Bound of the parts on mma.sync: instructions (counted for a warp's 16 target
+// tokens: 662 with 16 rows, 523 with 8; 572 and 450 for draft tokens; a good part of
+// them unpacks codes) and, in small calls, latency: 2 queries over 2048 + 128 draft
+// tokens take 7.1 us with the join, 16 x 8 caches of 0 to 1024 target tokens 19 us
+// with it (17 MB, 2.6 us to read).
 #include "launch.h"
 #include "nested_mma.cuh"
 #include "prefix_plan.h"

@@ -21,9 +21,12 @@
 // weights that the output before has used up.
 //
 // Measured: 128 x 4 queries of 32 heads over 16384 target tokens (8192 units, 56 a
-// CTA) 205 us, 667 TFLOP/s, about 6000 cycles a unit: its MMAs need 2048, its
-// exponentials 2048 (16 a cycle and SM); the SM's load/store pipe, which tensor
-// memory reads and writes, scales and operands share, is busy 80 % of the time.
+// CTA) 235 us with the join, 585 TFLOP/s.  Under the profiler (252 us) a unit takes
+// 7470 cycles: its MMAs need 3072, its exponentials 2048 (16 a cycle and SM), and no
+// unit is full: the SM's load/store pipe, which tensor memory reads and writes, scales
+// and operands share, 69 %, issue slots 52 %, tensor cores 41 %.  Without the second
+// terms' MMAs it is 3 % faster: what bounds it is the chain from scores to weights to
+// output of each half tile.
 // Scores held in registers for both passes by fewer warps were slower.
 //
 // The codes are exact in fp16, so a score is off by fp32 sums only.  The

@@ -519,7 +519,8 @@ int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t 
  *                    contents do not matter.  Calls that run at the same time
  *                    need scratch of their own (two graphs too, if they may).
  * D must be 128, H / Hkv one of 1, 2, 4, 8; scores |q k_t| / sqrt(128) below
- * 2^22.  Made for the L of decoding (one token, or a draft's few dozen): any L
+ * 2^22 (weights are as exact as fp32 holds scores and lse: some 2^-22 of the
+ * greatest).  Made for the L of decoding (one token, or a draft's few dozen): any L
  * is right, but own tokens are read once for each 16 rows (L H / Hkv of them),
  * so a whole prompt's own attention is far from fast here.  The prefix is attended by all
  * B * L * H / Hkv rows of a KV head together; its planes are read once for

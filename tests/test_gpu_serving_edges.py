@@ -166,6 +166,61 @@ def test_prefix_attention_keeps_the_weights_bits(shape, mode):
     assert np.all(np.abs(got - out) <= tol)
 
 
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("shape", [(64, 1, 8, 1, 700, 0), (1, 1, 8, 1, 700, 0), (2, 4, 8, 1, 0, 700)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_prefix_attention_of_the_greatest_scores(shape, mode):
+    """Scores just below 2^22, where fp32 steps by 1/4 and 1/2: finite outputs, to
+    which only the tokens of the greatest score add."""
+    B, L, H, Hkv, P, cap = shape
+    a = Attend(*shape, [cap] * B)
+    rng = np.random.default_rng(0)
+    n = P or cap
+    a.q = np.zeros((B, L, H, 128), np.float16)
+    a.q[..., 0] = 60000.0
+    rows = (P, Hkv) if P else (B, cap, Hkv)
+    code = rng.integers(1, 8, n)
+    code[[0, n // 2]] = 7
+    hi = np.full((n, 64), 0x88, np.uint8)
+    hi[:, 0] = 0x80 | (8 + code)
+    hi = np.broadcast_to(hi.reshape((1,) * (len(rows) - 2) + (n, 1, 64)), (*rows, 64)).copy()
+    scale = np.float16(112.5)  # 60000 * 7 * 112.5 / sqrt(128) = 4.18e6
+    k = hi, np.full_like(hi, 0x88), np.full(rows, scale, np.float16)
+    if P:
+        a.prefix[0] = k
+    else:
+        a.own[0] = k
+    a.upload()
+    out, lse, size = ref.attention(mode, a.q, a.prefix, a.own, a.lens)
+    assert 2.0 ** 21.9 < lse.max() < 2.0 ** 22
+    got = bn.prefix_attention(mode, *a.d)
+    # Equal scores have equal roundings and the next is 6e5 below, so within a part of the
+    # tokens weights are exact but for their two terms' 2^-22 and a few roundings.  Parts
+    # join by their lse in fp32 (log 2): half a step is 2^-24 of it, so a part's weight is
+    # off by a factor of at most exp(2^-24 lse), two parts' ratio by its square (1.65 here).
+    # lse: three roundings of the score.
+    part = np.expm1(2 * 2.0 ** -24 * lse)[..., None]
+    assert np.all(np.abs(host(got[0]).astype(np.float64) - out)
+                  <= (part + 2.0 ** -18) * size + 2.0 ** -11 * np.abs(out) + 2.0 ** -25)
+    assert np.all(np.abs(host(got[1]) - lse) <= 2.0 ** -21 * np.abs(lse))
+
+
+def test_lengths_past_the_cache_count_as_the_whole_cache():
+    """Several queries a sequence: attention, weights and eviction alike."""
+    B, L, H, Hkv, cap = 2, 3, 8, 2, 20
+    a = Attend(B, L, H, Hkv, 30, cap, [cap, cap])
+    longer = dev(np.array([cap + 5, 2 ** 31 - 1], np.int32))
+    want = bn.prefix_attention(1, *a.d)
+    got = bn.prefix_attention(1, *a.d[:3], longer)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    acc = [bn.kv_weights(1, a.d[0], want[1], a.d[2][0], torch.zeros(B, Hkv, cap, device="cuda"), n)
+           for n in (a.d[3], longer)]
+    assert torch.equal(*acc)
+    kept = [bn.kv_evict(acc[0], n, 7, 2, 2, *a.d[2], *bn.nested_cache(7, Hkv, B),
+                        torch.zeros(B, Hkv, 7, device="cuda")) for n in (a.d[3], longer)]
+    assert torch.equal(kept[0][0], kept[1][0]) and torch.equal(kept[0][1], kept[1][1])
+
+
 # ----------------------------------------------------------------- weights
 def _check_weights(mode, q, lse, k, acc, lens, got):
     """test_gpu_serving's bound: each weight off by the score's error and roundings

@@ -520,13 +520,13 @@ int bitnest_kv_read(int mode, const bitnest_kv_cache *cache, int64_t B, int64_t 
  *                    need scratch of their own (two graphs too, if they may).
  * D must be 128, H / Hkv one of 1, 2, 4, 8; scores |q k_t| / sqrt(128) below
  * 2^22 (weights are as exact as fp32 holds scores and lse: some 2^-22 of the
- * greatest).  Made for the L of decoding (one token, or a draft's few dozen): any L
- * is right, but own tokens are read once for each 16 rows (L H / Hkv of them),
- * so a whole prompt's own attention is far from fast here.  The prefix is attended by all
- * B * L * H / Hkv rows of a KV head together; its planes are read once for
- * them, not once for each sequence.  Scores, statistics and sums are fp32; each
- * p * v_scale enters its product as two fp16 terms (22 bits), and the output
- * is rounded to fp16.  Results do not depend on timing.
+ * greatest).  Made for the L of decoding (one token, or a draft's few dozen):
+ * any L is right, but own tokens are read once for each 16 rows (L H / Hkv of
+ * them), so a whole prompt's own attention is far from fast here.  The prefix
+ * is attended by all B * L * H / Hkv rows of a KV head together; its planes
+ * are read once for them, not once for each sequence.  Scores, statistics and
+ * sums are fp32; each p * v_scale enters its product as two fp16 terms (22
+ * bits), and the output is rounded to fp16.  Results do not depend on timing.
  */
 int64_t bitnest_prefix_attention_ws_bytes(int64_t B, int64_t L, int64_t H, int64_t Hkv, int64_t P,
                                           int64_t cap);
